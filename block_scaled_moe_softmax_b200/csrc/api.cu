@@ -13,13 +13,18 @@
 #include <string>
 
 #include "../../include/moe_mx.h"
+#include "host.cuh"
 #include "kernels.cuh"
 
 using namespace moe_mx;
 
 namespace {
-
 thread_local std::string g_last_error;
+} // namespace
+
+namespace moe_mx {
+
+void clear_error() { g_last_error.clear(); }
 
 int fail(int code, const char *fmt, ...)
 {
@@ -36,6 +41,10 @@ int cuda_fail(cudaError_t e, const char *what)
 {
     return fail(MOE_MX_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
+
+} // namespace moe_mx
+
+namespace {
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -54,10 +63,10 @@ EncodeTiledFn get_encode_fn()
     return fn;
 }
 
-// 2-D row-major tensor map: inner dimension `cols` elements, `rows` rows,
-// `row_bytes` bytes from one row to the next.
-// Tensor map of `rank` dimensions (innermost first): dims in elements, strides in bytes of
-// dimensions 1..rank-1, box in elements; 128-byte swizzle.
+} // namespace
+
+namespace moe_mx {
+
 int encode_nd(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *ptr, const cuuint64_t *dims,
               const cuuint64_t *strides, const cuuint32_t *box)
 {
@@ -72,6 +81,10 @@ int encode_nd(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *pt
         return fail(MOE_MX_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d, rank %d)", (int)r, rank);
     return MOE_MX_OK;
 }
+
+} // namespace moe_mx
+
+namespace {
 
 // 2-D row-major map: `cols` elements per row, `rows` rows, `row_bytes` from one row to the next.
 int encode_2d(CUtensorMap *map, CUtensorMapDataType dt, uint64_t row_bytes, const void *ptr, uint64_t cols,
@@ -92,6 +105,10 @@ int encode_act(CUtensorMap *map, const void *ptr, uint64_t K, uint64_t plane_row
     const cuuint32_t box[3] = {128, box_rows, terms};
     return encode_nd(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, ptr, dims, strides, box);
 }
+
+} // namespace
+
+namespace moe_mx {
 
 bool is_device_ptr(const void *p, int dev)
 {
@@ -116,7 +133,9 @@ int check_ptr(const void *p, int dev, const char *name)
     return MOE_MX_OK;
 }
 
-int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+} // namespace moe_mx
+
+namespace {
 
 // forwards of at most this many tokens write and read the activation scales in the N layout
 constexpr int kScalesNTokens = 16;

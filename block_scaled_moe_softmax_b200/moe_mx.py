@@ -40,6 +40,13 @@ MOE_MX_INTER_ASF = 1
 MOE_MX_INTER_HQ = 2
 MOE_MX_INTER_HSF = 3
 MOE_MX_INTER_Y = 4
+MOE_MX_TYPE_BF16 = 0
+MOE_MX_TYPE_F32 = 1
+MOE_MX_TYPE_F16 = 2
+MOE_MX_LINEAR_NONE = 0
+MOE_MX_LINEAR_SILU = 1
+MOE_MX_LINEAR_GELU = 2
+MOE_MX_LINEAR_SWIGLU = 3
 
 # Every symbol include/moe_mx.h declares: name -> (restype, argtypes)
 _P, _I, _I64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
@@ -65,6 +72,13 @@ SIGNATURES = {
     "moe_mx_get_intermediate": (_I, [_P, _I, _P, _P]),
     "moe_mx_launch_count": (ctypes.c_longlong, [_P]),
     "moe_mx_debug_encode_act": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_mx_dispatch": (_I, [_P, _I, _I, _I, _P, _I64, _I, _P, _P]),
+    "moe_mx_combine": (_I, [_P, _I64, _I, _I, _I, _P, _P, _I, _I, _P, _P]),
+    "moe_mx_combine_backward": (_I, [_P, _P, _I64, _I, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
+    "moe_mx_linear": (_I, [_P] * 6 + [_I, _I64] + [_I] * 5 + [_P, _P, _P, _I64, _P]),
+    "moe_mx_linear_workspace": (_I64, [_I, _I64] + [_I] * 5),
+    "moe_mx_linear_backward": (_I, [_P] * 6 + [_I, _I64] + [_I] * 5 + [_P, _P, _P, _P, _I64, _P]),
+    "moe_mx_linear_backward_workspace": (_I64, [_I, _I64] + [_I] * 5),
 }
 STAGES = ("route", "gather", "fc1", "fc2", "combine")
 
@@ -234,6 +248,61 @@ def moe_mx_get_stage_times(handle: int) -> dict:
     ms = (ctypes.c_float * len(STAGES))()
     _check(load_library().moe_mx_get_stage_times(handle, ctypes.cast(ms, ctypes.c_void_p)))
     return dict(zip(STAGES, [float(v) for v in ms]))
+
+
+# ------------------------------------------------------------------ routed operators
+# (block_scaled_moe_softmax_b200.routed_ops calls these on torch tensors)
+def moe_mx_dispatch(x, num_tokens: int, hidden: int, top_k: int, pos_of_pair, rows: int, dtype: int, grouped,
+                    stream=None) -> None:
+    _check(load_library().moe_mx_dispatch(_ptr(x), num_tokens, hidden, top_k, _ptr(pos_of_pair), rows, dtype,
+                                          _ptr(grouped), _stream(stream)))
+
+
+def moe_mx_combine(grouped, rows: int, num_tokens: int, hidden: int, top_k: int, pos_of_pair, topk_w, dtype: int,
+                   out_dtype: int, out, stream=None) -> None:
+    _check(load_library().moe_mx_combine(_ptr(grouped), rows, num_tokens, hidden, top_k, _ptr(pos_of_pair),
+                                         _ptr(topk_w), dtype, out_dtype, _ptr(out), _stream(stream)))
+
+
+def moe_mx_combine_backward(dout, grouped, rows: int, num_tokens: int, hidden: int, top_k: int, pos_of_pair, topk_w,
+                            topk_ids, num_experts: int, dtype: int, dout_dtype: int, dgrouped, dtopk_w, dlogits,
+                            stream=None) -> None:
+    _check(load_library().moe_mx_combine_backward(
+        _ptr(dout), _ptr(grouped), rows, num_tokens, hidden, top_k, _ptr(pos_of_pair), _ptr(topk_w), _ptr(topk_ids),
+        num_experts, dtype, dout_dtype, _ptr(dgrouped), _ptr(dtopk_w), _ptr(dlogits), _stream(stream)))
+
+
+def _checked_bytes(n: int) -> int:
+    if n < 0:
+        _check(n)
+    return n
+
+
+def moe_mx_linear_workspace(num_experts: int, rows: int, N: int, K: int, dtype: int, activation: int,
+                            out_dtype: int) -> int:
+    return _checked_bytes(load_library().moe_mx_linear_workspace(num_experts, rows, N, K, dtype, activation,
+                                                                 out_dtype))
+
+
+def moe_mx_linear_backward_workspace(num_experts: int, rows: int, N: int, K: int, dtype: int, activation: int,
+                                     dout_dtype: int) -> int:
+    return _checked_bytes(load_library().moe_mx_linear_backward_workspace(num_experts, rows, N, K, dtype, activation,
+                                                                          dout_dtype))
+
+
+def moe_mx_linear(x, w, bias, residual, counts, pad_offsets, num_experts: int, rows: int, N: int, K: int, dtype: int,
+                  activation: int, out_dtype: int, out, preact, workspace, workspace_bytes: int, stream=None) -> None:
+    _check(load_library().moe_mx_linear(
+        _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(counts), _ptr(pad_offsets), num_experts, rows, N, K, dtype,
+        activation, out_dtype, _ptr(out), _ptr(preact), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def moe_mx_linear_backward(dout, x, w, preact, counts, pad_offsets, num_experts: int, rows: int, N: int, K: int,
+                           dtype: int, activation: int, dout_dtype: int, dx, dw, dbias, workspace,
+                           workspace_bytes: int, stream=None) -> None:
+    _check(load_library().moe_mx_linear_backward(
+        _ptr(dout), _ptr(x), _ptr(w), _ptr(preact), _ptr(counts), _ptr(pad_offsets), num_experts, rows, N, K, dtype,
+        activation, dout_dtype, _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 # ------------------------------------------------------------------ convenience wrappers

@@ -470,6 +470,124 @@ MOE_MX_API int moe_mx_route_group_noalloc(const float *router_logits, int num_to
                                           int32_t *topk_ids, float *topk_w, int32_t *counts, int32_t *pad_offsets,
                                           int32_t *sorted_pair, int32_t *pos_of_pair, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Routed operators: what a layer around or beside moe_mx_forward needs -- the router's product, token
+ * rows moved to the grouped layout of moe_mx_route_group_noalloc and back, products of unquantised
+ * experts, and the gradients of each, for training.  Together:
+ *   logits = linear(x, w_router)          -> moe_mx_route_group_noalloc
+ *   grouped = dispatch(x)                 h = linear(grouped, w1[e], swiglu)
+ *   y = linear(h, w2[e])                  out = combine(y, topk_w)
+ * They need no handle, allocate nothing, keep nothing between calls, and may be captured in a CUDA
+ * graph.  A call runs on the device that holds its first tensor; `stream` is a stream of that
+ * device.  Calls on different streams do not disturb one another as long as their output and
+ * workspace buffers differ.  No atomics: equal inputs give equal bits.
+ *
+ * Grouped layout: grouped buffers have `rows` rows (at least pad_offsets[E]); expert e's rows are
+ * pad_offsets[e] .. pad_offsets[e] + counts[e] - 1, pad_offsets[e] being multiples of 128 in
+ * ascending order.  The other rows are padding: never read into a result, never written.
+ * Dimensions (hidden, N, K): 1..2^20, odd ones included (multiples of 8 are fastest).
+ * ------------------------------------------------------------------------- */
+
+/* Element types of the routed operators' tensors. */
+#define MOE_MX_TYPE_BF16 0
+#define MOE_MX_TYPE_F32 1
+#define MOE_MX_TYPE_F16 2
+
+/* Activations of moe_mx_linear. */
+#define MOE_MX_LINEAR_NONE 0
+#define MOE_MX_LINEAR_SILU 1   /* z * sigmoid(z) */
+#define MOE_MX_LINEAR_GELU 2   /* tanh form: 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+#define MOE_MX_LINEAR_SWIGLU 3 /* silu(z[:, :N/2]) * z[:, N/2:]: gate rows of w, then up rows */
+
+/*
+ * Token rows to their pairs' grouped rows: grouped[pos_of_pair[t*k + j]] = x[t].
+ *   x            [T, H] of dtype (any MOE_MX_TYPE_*); T = 0 enqueues nothing.
+ *   pos_of_pair  int32 [T*k] grouped row of each pair, all different; a row outside [0, rows) (a
+ *                pair of another shard's expert) is left out.
+ *   grouped      [rows, H] of dtype; only the pairs' rows are written.  Must not overlap x.
+ * The gradient of dispatch is moe_mx_combine without weights.
+ * Errors: INVALID_ARG, CUDA.
+ */
+MOE_MX_API int moe_mx_dispatch(const void *x, int num_tokens, int hidden, int top_k, const int32_t *pos_of_pair,
+                               int64_t rows, int dtype, void *grouped, void *stream);
+
+/*
+ * Grouped rows back to their tokens: out[t] = sum_j topk_w[t,j] * grouped[pos_of_pair[t*k + j]], j
+ * ascending, in float32, rounded once.
+ *   grouped   [rows, H] of dtype; out [T, H] of out_dtype, written (a token without a pair in
+ *             [0, rows): zero).  out must not overlap grouped.
+ *   topk_w    float32 [T, k], or NULL: every weight 1 (the gradient of dispatch).
+ * Errors: INVALID_ARG, CUDA.
+ */
+MOE_MX_API int moe_mx_combine(const void *grouped, int64_t rows, int num_tokens, int hidden, int top_k,
+                              const int32_t *pos_of_pair, const float *topk_w, int dtype, int out_dtype, void *out,
+                              void *stream);
+
+/*
+ * Gradient of moe_mx_combine with weights, and of the router's weights.  With r = pos_of_pair[t*k + j]:
+ *   dgrouped [rows, H] of dtype, or NULL:  dgrouped[r] = topk_w[t,j] * dout[t] (padding rows are left
+ *            as they were); must not overlap dout or grouped.
+ *   dtopk_w  float32 [T, k], or NULL:      <dout[t], grouped[r]> (0 for a pair left out).
+ *   dlogits  float32 [T, num_experts], or NULL: the gradient through topk_w = softmax over the k chosen
+ *            logits, which is what the router computes: dlogits[t, topk_ids[t,j]] = topk_w[t,j] *
+ *            (dtopk_w[t,j] - sum_i topk_w[t,i] dtopk_w[t,i]), 0 for an expert not chosen (an id outside
+ *            [0, num_experts) is not written; one that a token holds twice adds up).
+ *   dout [T, H] of dout_dtype; grouped [rows, H] as given to combine (may be NULL when only dgrouped is
+ *   asked for); topk_ids int32 [T, k], num_experts 1..1024: with dlogits only.
+ * Sums are float32 in a fixed order.  Errors: INVALID_ARG, CUDA.
+ */
+MOE_MX_API int moe_mx_combine_backward(const void *dout, const void *grouped, int64_t rows, int num_tokens,
+                                       int hidden, int top_k, const int32_t *pos_of_pair, const float *topk_w,
+                                       const int32_t *topk_ids, int num_experts, int dtype, int dout_dtype,
+                                       void *dgrouped, float *dtopk_w, float *dlogits, void *stream);
+
+/*
+ * out = act(x w^T + bias) + residual, with float32 accumulation and one rounding of each output.
+ *   num_experts  0: dense; x [rows, K], w [N, K], bias [N].
+ *                E in 1..1024: the rows are in the grouped layout, w [E, N, K], bias [E, N]; counts
+ *                int32 [E] and pad_offsets int32 [E+1] (device) give the segments.  NULL when dense.
+ *   dtype        of x, w and preact: MOE_MX_TYPE_BF16 or MOE_MX_TYPE_F16.
+ *   bias         float32, or NULL.     activation  MOE_MX_LINEAR_*.
+ *   out_dtype    of out and residual: dtype or MOE_MX_TYPE_F32.
+ *   out          [rows, N], or [rows, N/2] for SWIGLU.
+ *   residual     like out, or NULL; may be out itself.
+ *   preact       [rows, N] or NULL: x w^T + bias rounded to dtype, as moe_mx_linear_backward takes it.
+ *   workspace    device buffer of at least moe_mx_linear_workspace(...) bytes (NULL if that is 0), 16-byte
+ *                aligned, used until the call's work is done: calls that may run at the same time, and
+ *                captured graphs that may, need one each.
+ * rows = 0 enqueues nothing.  Errors: INVALID_ARG, CUDA.
+ */
+MOE_MX_API int moe_mx_linear(const void *x, const void *w, const float *bias, const void *residual,
+                             const int32_t *counts, const int32_t *pad_offsets, int num_experts, int64_t rows, int N,
+                             int K, int dtype, int activation, int out_dtype, void *out, void *preact,
+                             void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Workspace bytes of moe_mx_linear for these sizes (host arithmetic; a negative status if invalid). */
+MOE_MX_API int64_t moe_mx_linear_workspace(int num_experts, int64_t rows, int N, int K, int dtype, int activation,
+                                           int out_dtype);
+
+/*
+ * Gradient of moe_mx_linear (its residual's gradient is dout itself).  dz = dout * act'(preact):
+ *   dx     [rows, K] of dtype, or NULL:     dz w (padding rows are left as they were);
+ *   dw     [N, K] or [E, N, K] of dtype, or NULL: dz^T x, written (an expert without rows: zero);
+ *   dbias  float32 [N] or [E, N], or NULL:  sum over the rows of dz, before dz is rounded.
+ * The two products take dz rounded to dtype, the type of x and w; they accumulate in float32.
+ *   dout   [rows, N], or [rows, N/2] for SWIGLU, of dout_dtype: dtype or MOE_MX_TYPE_F32.
+ *   preact as moe_mx_linear wrote it; NULL for MOE_MX_LINEAR_NONE.
+ *   x, w, counts, pad_offsets, num_experts, rows, N, K, dtype, activation: as for moe_mx_linear (x is
+ *   read for dw only, w for dx only).  workspace: moe_mx_linear_backward_workspace(...) bytes.
+ * rows = 0 writes dw and dbias as zeros.  Errors: INVALID_ARG, CUDA.
+ */
+MOE_MX_API int moe_mx_linear_backward(const void *dout, const void *x, const void *w, const void *preact,
+                                      const int32_t *counts, const int32_t *pad_offsets, int num_experts,
+                                      int64_t rows, int N, int K, int dtype, int activation, int dout_dtype,
+                                      void *dx, void *dw, float *dbias, void *workspace, int64_t workspace_bytes,
+                                      void *stream);
+
+/* Workspace bytes of moe_mx_linear_backward (host arithmetic; a negative status if invalid). */
+MOE_MX_API int64_t moe_mx_linear_backward_workspace(int num_experts, int64_t rows, int N, int K, int dtype,
+                                                    int activation, int dout_dtype);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,466 @@
+"""The routed operators (dispatch, combine, linear and their gradients) against plain float64 code."""
+import math
+
+import pytest
+import torch
+
+from block_scaled_moe_softmax_b200 import moe_mx
+from tests import routed_ref as ref
+
+ops = pytest.importorskip("block_scaled_moe_softmax_b200.routed_ops")
+pytestmark = pytest.mark.gpu
+BF, HF, F = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+
+
+def rnd(shape, dtype, seed, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def untouched(buf, written, fill):
+    """Rows of a grouped buffer that hold no pair keep the fill."""
+    keep = torch.ones(buf.shape[0], dtype=torch.bool, device=buf.device)
+    keep[written] = False
+    assert torch.equal(buf[keep], torch.full_like(buf[keep], fill))
+
+
+# ---------------------------------------------------------------- dispatch and combine
+PERMUTE = [  # T, E, k, H, drop, hot
+    (1, 1, 1, 8, 0.0, None), (1, 8, 2, 1, 0.0, None), (16, 8, 2, 256, 0.0, None), (7, 5, 3, 33, 0.3, None),
+    (300, 60, 6, 1000, 0.1, None), (130, 4, 2, 130, 0.0, 1), (64, 40, 32, 72, 0.5, None), (3, 8, 2, 7168, 0.0, None),
+    (5, 9, 9, 2056, 1.0, None),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F])
+@pytest.mark.parametrize("T,E,k,H,drop,hot", PERMUTE)
+def test_dispatch_copies_every_pair(T, E, k, H, drop, hot, dtype):
+    r = ref.make_routing(T, E, k, 1, drop, hot)
+    x = rnd((T, H), dtype, 2)
+    out = torch.full((r.rows, H), 7.0, dtype=dtype, device="cuda")
+    assert ops.dispatch(x, r, out=out) is out
+    pos = r.pos_of_pair.long()
+    tok = torch.arange(T * k, device="cuda") // k
+    assert torch.equal(out[pos[pos >= 0]], x[tok[pos >= 0]])
+    untouched(out, pos[pos >= 0], 7.0)
+
+
+def _combine64(y, r, weighted):
+    T, k = r.topk_w.shape
+    pos = r.pos_of_pair.long().view(T, k)
+    live = (pos >= 0)[..., None]
+    rows = torch.where(live, y[pos.clamp(min=0)].to(ref.F64), 0.0)
+    w = r.topk_w.to(ref.F64)[..., None] if weighted else 1.0
+    return (rows * w).sum(1), (rows * w).abs().sum(1) * (k + 1) * 2.0 ** -23
+
+
+@pytest.mark.parametrize("weighted", [True, False])
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (HF, F), (F, BF), (F, F), (BF, HF)])
+@pytest.mark.parametrize("T,E,k,H,drop,hot", PERMUTE)
+def test_combine_sums_every_pair(T, E, k, H, drop, hot, dtype, out, weighted):
+    r = ref.make_routing(T, E, k, 3, drop, hot)
+    y = torch.full((r.rows, H), math.nan, dtype=dtype, device="cuda")  # padding must not be read
+    pos = r.pos_of_pair.long()
+    y[pos[pos >= 0]] = rnd((int((pos >= 0).sum()), H), dtype, 4)
+    got = (ops.combine if weighted else ops.dispatch_backward)(y, r, out_dtype=out)
+    assert got.dtype == out
+    ref.close(got, *_combine64(y, r, weighted), "combine")
+
+
+@pytest.mark.parametrize("dtype,dout_t", [(BF, BF), (HF, F), (F, BF), (F, F)])
+@pytest.mark.parametrize("T,E,k,H,drop,hot", PERMUTE)
+def test_combine_backward(T, E, k, H, drop, hot, dtype, dout_t):
+    r = ref.make_routing(T, E, k, 5, drop, hot)
+    pos = r.pos_of_pair.long()
+    live = pos[pos >= 0]
+    y = torch.full((r.rows, H), math.nan, dtype=dtype, device="cuda")
+    y[live] = rnd((len(live), H), dtype, 6)
+    dout = rnd((T, H), dout_t, 7)
+    dy = torch.full((r.rows, H), 7.0, dtype=dtype, device="cuda")
+    got_dy, dw, dlogits = ops.combine_backward(dout, y, r, num_experts=E, dy=dy)
+    assert got_dy is dy
+    tok = torch.arange(T * k, device="cuda") // k
+    d64, w64 = dout.to(ref.F64), r.topk_w.to(ref.F64)
+    want = d64[tok] * w64.reshape(-1, 1)
+    ref.close(dy[live], want[pos >= 0], want[pos >= 0].abs() * 2.0 ** -24, "dy")
+    untouched(dy, live, 7.0)
+    rows = torch.where((pos >= 0)[:, None], y[pos.clamp(min=0)].to(ref.F64), 0.0)
+    prod = d64[tok] * rows
+    want_dw, dw_b = prod.sum(1).view(T, k), prod.abs().sum(1).view(T, k) * (H + 2) * 2.0 ** -23
+    ref.close(dw, want_dw, dw_b, "dw")
+    # the softmax's gradient on what it is given: the bound follows dw's through the two sums
+    g = w64 * (want_dw - (w64 * want_dw).sum(1, keepdim=True))
+    size = want_dw.abs() + dw_b
+    g_b = w64 * (dw_b + (w64 * dw_b).sum(1, keepdim=True) + (k + 4) * 2.0 ** -23 * (size + (w64 * size).sum(1, keepdim=True)))
+    ids = r.topk_ids.long()
+    zero = torch.zeros(T, E, dtype=ref.F64, device="cuda")
+    ref.close(dlogits, zero.scatter_add(1, ids, g), zero.scatter_add(1, ids, g_b), "dlogits")
+    assert torch.equal(dlogits[zero.scatter_add(1, ids, torch.ones_like(g)) == 0],
+                       torch.zeros_like(dlogits[zero.scatter_add(1, ids, torch.ones_like(g)) == 0]))
+
+
+def test_rows_and_ids_out_of_range_are_left_out():
+    T, E, k, H = 4, 4, 2, 64
+    r = ref.make_routing(T, E, k, 8)
+    pos = r.pos_of_pair.clone()
+    pos[0], pos[3] = r.rows, 2 ** 31 - 1  # behind the buffer
+    bad = r._replace(pos_of_pair=pos)
+    x = rnd((T, H), BF, 9)
+    out = torch.zeros(r.rows, H, dtype=BF, device="cuda")
+    ops.dispatch(x, bad, out=out)
+    kept = [p for p in range(T * k) if p not in (0, 3)]
+    want = torch.zeros_like(out)
+    want[r.pos_of_pair.long()[kept]] = x[[p // k for p in kept]]
+    assert torch.equal(out, want)
+    dropped = pos.clone()
+    dropped[[0, 3]] = -1
+    ref.close(ops.combine(out, bad), *_combine64(out, r._replace(pos_of_pair=dropped), True), "combine")
+    # a token that holds an expert twice, and ids outside the logits
+    ids = r.topk_ids.clone()
+    ids[0] = 2
+    ids[1, 0], ids[2, 1] = -1, E
+    dout = rnd((T, H), BF, 10)
+    _, dw, dl = ops.combine_backward(dout, out, bad._replace(topk_ids=ids), num_experts=E)
+    w = r.topk_w.to(ref.F64)
+    g = w * (dw.to(ref.F64) - (w * dw.to(ref.F64)).sum(1, keepdim=True))
+    want = torch.zeros(T, E, dtype=ref.F64, device="cuda")
+    for t in range(T):
+        for j in range(k):
+            if 0 <= int(ids[t, j]) < E:
+                want[t, int(ids[t, j])] += g[t, j]
+    ref.close(dl, want, (w * dw.abs()).sum(1, keepdim=True) * 8 * 2.0 ** -23 + 0 * want, "dlogits")
+
+
+# ---------------------------------------------------------------- linear
+ACTS = ["none", "silu", "gelu", "swiglu"]
+DENSE = [  # M, N, K
+    (1, 1, 1), (1, 384, 512), (2, 10, 7), (16, 512, 1024), (17, 130, 200), (33, 64, 72), (64, 264, 136),
+    (65, 130, 321), (127, 257, 96), (128, 128, 64), (129, 384, 640), (256, 512, 192), (300, 1000, 333),
+    (515, 770, 264), (1024, 96, 2048),
+]
+
+
+def _linear_inputs(M, N, K, dtype, out, act, bias, residual, seed, E=0):
+    cols = N // 2 if act == "swiglu" else N
+    x = rnd((M, K), dtype, seed)
+    w = rnd(((E,) if E else ()) + (N, K), dtype, seed + 1, K ** -0.5)
+    b = rnd(((E,) if E else ()) + (N,), F, seed + 2) if bias else None
+    res = rnd((M, cols), out, seed + 3) if residual else None
+    return x, w, b, res, cols
+
+
+def _check_linear(x, w, b, res, act, out, r=None, preact=True):
+    rows, N = x.shape[0], w.shape[-2]
+    pre = torch.full((rows, N), 7.0, dtype=x.dtype, device="cuda") if preact else None
+    cols = N // 2 if act == "swiglu" else N
+    buf = torch.full((rows, cols), 7.0, dtype=out, device="cuda")
+    got = ops.linear(x, w, b, residual=res, activation=act, routing=r, out=buf, preact=pre)
+    want, want_pre, bound, pre_bound = ref.linear64(x, w, b, res, act, r)
+    ref.close(got, want, bound, "out")
+    ref.close_norm(got, want, 1, "out")
+    if preact:
+        ref.close(pre, want_pre, pre_bound, "preact")
+        ref.close_norm(pre, want_pre, 1, "preact")
+    if r is not None:
+        live = r.pos_of_pair.long()
+        untouched(got, live[live >= 0], 7.0)
+        if preact:
+            untouched(pre, live[live >= 0], 7.0)
+
+
+@pytest.mark.parametrize("M,N,K", DENSE)
+@pytest.mark.parametrize("act,bias,residual,dtype,out", [
+    ("none", False, False, BF, BF), ("none", True, True, BF, F), ("silu", True, False, HF, HF),
+    ("gelu", False, True, BF, BF), ("swiglu", True, True, HF, F), ("swiglu", False, False, BF, BF)])
+def test_linear_dense(M, N, K, act, bias, residual, dtype, out):
+    N += N % 2 if act == "swiglu" else 0
+    x, w, b, res, _ = _linear_inputs(M, N, K, dtype, out, act, bias, residual, 11)
+    _check_linear(x, w, b, res, act, out)
+
+
+GROUPED = [  # T, E, k, N, K, drop, hot
+    (1, 1, 1, 64, 64, 0.0, None), (5, 6, 2, 40, 24, 0.0, None), (200, 3, 1, 96, 80, 0.2, None),
+    (300, 8, 2, 256, 136, 0.0, 2), (700, 5, 2, 130, 70, 0.0, 0), (64, 40, 8, 264, 128, 0.3, None),
+    (9, 6, 2, 66, 33, 1.0, None),
+]
+
+
+@pytest.mark.parametrize("T,E,k,N,K,drop,hot", GROUPED)
+@pytest.mark.parametrize("act,bias,residual,dtype,out", [
+    ("none", True, False, BF, BF), ("swiglu", True, False, BF, BF), ("gelu", False, True, HF, F)])
+def test_linear_grouped(T, E, k, N, K, drop, hot, act, bias, residual, dtype, out):
+    r = ref.make_routing(T, E, k, 12, drop, hot)
+    x, w, b, res, _ = _linear_inputs(r.rows, N, K, dtype, out, act, bias, residual, 13, E)
+    pos = r.pos_of_pair.long()
+    pad = torch.ones(r.rows, dtype=torch.bool, device="cuda")
+    pad[pos[pos >= 0]] = False
+    x[pad] = math.nan  # padding must not reach a result
+    _check_linear(x, w, b, res, act, out, r)
+
+
+def _check_backward(dout, x, w, pre, act, r=None):
+    dx = torch.full(x.shape, 7.0, dtype=x.dtype, device="cuda")
+    got = ops.linear_backward(dout, x, w, pre, act, r, bias_grad=True, dx=dx)
+    want, bound = ref.linear_backward64(dout, x, w, pre, act, r)
+    for name, g, a, b in zip(("dx", "dw", "db"), got, want, bound):
+        ref.close(g, a, b, name)
+    # one rounding of dz and one of the output
+    ref.close_norm(got[0], want[0], 2, "dx")
+    ref.close_norm(got[1], want[1], 2, "dw")
+    if r is not None:
+        live = r.pos_of_pair.long()
+        untouched(dx, live[live >= 0], 7.0)
+    return got
+
+
+@pytest.mark.parametrize("M,N,K", DENSE)
+@pytest.mark.parametrize("act,dtype,dout_t", [("none", BF, BF), ("none", BF, F), ("silu", HF, HF), ("gelu", BF, F),
+                                              ("swiglu", BF, BF)])
+def test_linear_backward_dense(M, N, K, act, dtype, dout_t):
+    N += N % 2 if act == "swiglu" else 0
+    x, w, _, _, cols = _linear_inputs(M, N, K, dtype, dout_t, act, False, False, 14)
+    pre = rnd((M, N), dtype, 15) if act != "none" else None
+    _check_backward(rnd((M, cols), dout_t, 16), x, w, pre, act)
+
+
+@pytest.mark.parametrize("T,E,k,N,K,drop,hot", GROUPED)
+@pytest.mark.parametrize("act,dtype,dout_t", [("none", BF, BF), ("swiglu", HF, HF), ("silu", BF, F)])
+def test_linear_backward_grouped(T, E, k, N, K, drop, hot, act, dtype, dout_t):
+    r = ref.make_routing(T, E, k, 17, drop, hot)
+    x, w, _, _, cols = _linear_inputs(r.rows, N, K, dtype, dout_t, act, False, False, 18, E)
+    pre = rnd((r.rows, N), dtype, 19) if act != "none" else None
+    dout = rnd((r.rows, cols), dout_t, 20)
+    pos = r.pos_of_pair.long()
+    pad = torch.ones(r.rows, dtype=torch.bool, device="cuda")
+    pad[pos[pos >= 0]] = False
+    for t in (x, dout, pre):
+        if t is not None:
+            t[pad] = math.nan
+    dx, dw, db = _check_backward(dout, x, w, pre, act, r)
+    empty = r.counts == 0
+    assert not dw[empty].abs().sum() and not db[empty].abs().sum()
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_linear_backward_against_differences(act):
+    """<gradient, direction> against the float64 forward's central difference along the direction.  Each
+    gradient element is off by at most its bound and its rounding; the difference quotient of step h by
+    h^2 times a third derivative below 8 sum |terms| here."""
+    M, N, K = 40, 48, 56
+    x, w, b, _, cols = _linear_inputs(M, N, K, BF, BF, act, True, False, 21)
+    v = rnd((M, cols), BF, 22)
+    pre = torch.empty(M, N, dtype=BF, device="cuda")
+    ops.linear(x, w, b, activation=act, preact=pre)
+    dx, dw, db = ops.linear_backward(v, x, w, pre if act != "none" else None, act, bias_grad=True)
+    f = lambda x_, w_, b_: (ref.act64(x_ @ w_.t() + b_, act) * v.to(ref.F64)).sum()  # noqa: E731
+    x64, w64, b64 = x.to(ref.F64), w.to(ref.F64), b.to(ref.F64)
+    # preact is rounded to bf16: act' moves by at most 1.1 (silu'', gelu'' < 0.8, swiglu's cross terms 1.1) z u
+    z = x64 @ w64.t() + b64
+    if act == "swiglu":
+        g, up = z.chunk(2, -1)
+        dz_move = torch.cat([v.abs() * (up.abs() * 0.8 * g.abs() + 1.1 * up.abs()), v.abs() * 1.1 * g.abs()], -1) * ref.u(BF)
+    else:
+        dz_move = v.abs() * 0.8 * z.abs() * ref.u(BF) if act != "none" else 0 * z
+    _, (dxb, dwb, dbb) = ref.linear_backward64(v, x, w, pre if act != "none" else None, act)
+    h = 1e-4
+    for name, grad, bound, at, move in (
+            ("dx", dx, dxb, 0, dz_move.to(ref.F64) @ w64.abs()),
+            ("dw", dw, dwb, 1, dz_move.to(ref.F64).t() @ x64.abs()),
+            ("db", db, dbb, 2, dz_move.to(ref.F64).sum(0))):
+        d = rnd(grad.shape, F, 23 + at).to(ref.F64)
+        args = [x64, w64, b64]
+        lo, hi = list(args), list(args)
+        lo[at], hi[at] = args[at] - h * d, args[at] + h * d
+        want = float((f(*hi) - f(*lo)) / (2 * h))
+        got = float((grad.to(ref.F64) * d).sum())
+        tol = float(((bound + move + ref.u(grad.dtype) * grad.to(ref.F64).abs()) * d.abs()).sum())
+        assert abs(got - want) <= tol + 1e-3, f"{name}: {got} against {want}, tolerance {tol}"
+
+
+def test_no_tokens():
+    r = ref.make_routing(1, 4, 1, 24, drop=1.0)
+    empty = torch.empty(0, 64, dtype=BF, device="cuda")
+    w = rnd((32, 64), BF, 25)
+    assert ops.linear(empty, w).shape == (0, 32)
+    dx, dw, db = ops.linear_backward(torch.empty(0, 32, dtype=BF, device="cuda"), empty, w, bias_grad=True,
+                                     dw=torch.full_like(w, 7.0))
+    assert dx.shape == (0, 64) and not dw.abs().sum() and not db.abs().sum()
+    none = ops.route_group(torch.empty(0, 4, device="cuda"), 2)
+    assert none.rows == 0 and ops.dispatch(empty, none).shape == (0, 64)
+    assert ops.combine(torch.empty(0, 64, dtype=BF, device="cuda"), none).shape == (0, 64)
+    # every pair left out: the combine writes zeros
+    y = torch.full((r.rows, 64), math.nan, dtype=BF, device="cuda")
+    assert not ops.combine(y, r).abs().sum()
+
+
+def test_residual_in_place_and_infinities():
+    x, w, b, res, _ = _linear_inputs(40, 64, 72, BF, BF, "none", True, True, 26)
+    res[3, 5], res[4, 6] = math.inf, math.nan
+    want = ops.linear(x, w, b, residual=res)
+    got = ops.linear(x, w, b, residual=res, out=res)
+    assert got is res and torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got[~got.isnan()], want[~want.isnan()])
+    assert math.isinf(float(got[3, 5])) and got.isnan().sum() == 1
+    # a token with an infinity spoils its own row alone
+    x[7, 0] = math.inf
+    out = ops.linear(x, w, b)
+    assert not out[7].isfinite().any() and out[:7].isfinite().all() and out[8:].isfinite().all()
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_far_activations_are_their_limits(act):
+    """Activations and gradients at |z| of 1e2 and 1e30: the limits, no NaN from an overflowing power."""
+    n = 8
+    w = torch.eye(n, dtype=BF, device="cuda")
+    x = torch.tensor([[1e2, -1e2, 1e30, -1e30, 1.0, 1.0, 1.0, 1.0]], dtype=BF, device="cuda")
+    if act == "swiglu":
+        w = torch.cat([w, w.flip(0)])
+    pre = torch.empty(1, w.shape[0], dtype=BF, device="cuda")
+    out = ops.linear(x, w, activation=act, preact=pre)
+    assert out.isfinite().all()
+    dx, _, _ = ops.linear_backward(torch.ones_like(out), x, w, pre if act != "none" else None, act)
+    assert dx.isfinite().all()
+    if act in ("silu", "gelu"):
+        assert torch.equal(out[0, :4], x[0, :4].clamp(min=0)) and torch.equal(dx[0, :4].float(), torch.tensor([1., 0, 1, 0], device="cuda"))
+
+
+# ---------------------------------------------------------------- together
+def _stage_inputs(T=220, H=192, I=128, E=6, k=2):
+    return dict(x=rnd((T, H), BF, 31), wr=rnd((E, H), BF, 32, H ** -0.5), br=rnd((E,), F, 33),
+                w1=rnd((E, 2 * I, H), BF, 34, H ** -0.5), b1=rnd((E, 2 * I), F, 35), w2=rnd((E, H, I), BF, 36, I ** -0.5),
+                dout=rnd((T, H), BF, 37)), k
+
+
+def _layer(p, k):
+    """One training pass of a routed layer of unquantised experts on a residual stream: outputs and gradients."""
+    E = p["wr"].shape[0]
+    logits = ops.linear(p["x"], p["wr"], p["br"], out_dtype=F)
+    r = ops.route_group(logits, k)
+    g = ops.dispatch(p["x"], r)
+    z = torch.empty(r.rows, p["w1"].shape[1], dtype=BF, device="cuda")
+    h = ops.linear(g, p["w1"], p["b1"], activation="swiglu", routing=r, preact=z)
+    y = ops.linear(h, p["w2"], routing=r)
+    out = ops.combine(y, r)
+    dy, dw, dlogits = ops.combine_backward(p["dout"], y, r, num_experts=E)
+    dh, dw2, _ = ops.linear_backward(dy, h, p["w2"], routing=r)
+    dg, dw1, db1 = ops.linear_backward(dh, g, p["w1"], z, "swiglu", r, bias_grad=True)
+    dxr, dwr, dbr = ops.linear_backward(dlogits, p["x"], p["wr"], bias_grad=True)
+    dxe = ops.dispatch_backward(dg, r)
+    return dict(logits=logits, out=out, dw1=dw1, db1=db1, dw2=dw2, dwr=dwr, dbr=dbr, dxr=dxr, dxe=dxe), r
+
+
+def test_layer_and_its_gradients_together():
+    """Against float64 autograd of the whole layer with the same selection.  Relative errors in norm: the
+    values pass at most 8 roundings to bf16 in a row (x and w exact; g, z, h, y, dy, dh, dz, result),
+    each at most u, and the sums in between do not enlarge a relative error in norm for these random
+    operands by more than their condition, taken as 4."""
+    p, k = _stage_inputs()
+    got, r = _layer(p, k)
+    T, E = got["logits"].shape
+    leaf = {n: t.to(ref.F64).requires_grad_() for n, t in p.items() if n != "dout"}
+    logits = leaf["x"] @ leaf["wr"].t() + leaf["br"]
+    ids = r.topk_ids.long()
+    # the selection is the given one; it is the top-k of these logits, within their rounding
+    top = torch.topk(got["logits"], k, dim=1)
+    assert torch.equal(top.indices.sort(1).values, ids.sort(1).values)
+    w = torch.softmax(logits.gather(1, ids), 1)
+    z = torch.einsum("th,enh->ten", leaf["x"], leaf["w1"]) + leaf["b1"]
+    y = torch.einsum("tei,ehi->teh", ref.act64(z, "swiglu"), leaf["w2"])
+    out = (y[torch.arange(T, device="cuda")[:, None], ids] * w[..., None]).sum(1)
+    names = ["x", "wr", "br", "w1", "b1", "w2"]
+    grads = dict(zip(names, torch.autograd.grad(out, [leaf[n] for n in names], p["dout"].to(ref.F64))))
+    tol = 4 * 8 * ref.u(BF)
+    for name, g, want in (("logits", got["logits"], logits), ("out", got["out"], out), ("w1", got["dw1"], grads["w1"]),
+                          ("b1", got["db1"], grads["b1"]), ("w2", got["dw2"], grads["w2"]), ("wr", got["dwr"], grads["wr"]),
+                          ("br", got["dbr"], grads["br"]), ("x", got["dxr"].to(ref.F64) + got["dxe"].to(ref.F64), grads["x"])):
+        rel = float((g.to(ref.F64) - want.detach()).norm() / want.detach().norm())
+        assert rel <= tol, f"{name}: relative error {rel:.2e}"
+
+
+def test_layer_is_captured_replayed_and_repeats_its_bits():
+    p, k = _stage_inputs(T=300, H=256)
+    want, _ = _layer(p, k)
+    again, _ = _layer(p, k)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _layer(p, k)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got, _ = _layer(p, k)
+    other = rnd(p["x"].shape, BF, 38)
+    kept = p["x"].clone()
+    for x in (other, kept):  # new inputs, then the first ones again
+        p["x"].copy_(x)
+        graph.replay()
+    torch.cuda.synchronize()
+    for name in want:
+        assert torch.equal(again[name], want[name]), name
+        assert torch.equal(got[name], want[name]), name
+
+
+def test_two_streams_at_once():
+    p, k = _stage_inputs(T=257)
+    r = ref.make_routing(257, 6, 2, 39)
+    jobs = [lambda s=s: ops.linear_backward(p["dout"], p["x"], rnd((192, 192), BF, s), rnd((257, 192), BF, s + 1), "silu",
+                                            bias_grad=True) for s in (40, 50)]
+    want = [[t.clone() for t in j()] for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(5):
+        got = []
+        for j, s in zip(jobs, streams):
+            with torch.cuda.stream(s):
+                got.append(j())
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+    assert r.rows > 0
+
+
+def test_another_stream_is_used():
+    """A call with stream= runs there: it sees what that stream wrote before."""
+    s = torch.cuda.Stream()
+    x = torch.zeros(64, 512, dtype=BF, device="cuda")
+    w = rnd((32, 512), BF, 60)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        x.fill_(1.0)
+    out = ops.linear(x, w, stream=s)
+    s.synchronize()
+    ref.close(out, *[a for i, a in enumerate(ref.linear64(torch.ones_like(x), w, None, None, "none")) if i in (0, 2)], "out")
+
+
+def test_routing_of_the_library_feeds_the_operators():
+    T, E, k, H = 200, 32, 4, 128
+    logits = rnd((T, E), F, 61)
+    r = ops.route_group(logits, k)
+    x = rnd((T, H), BF, 62)
+    g = ops.dispatch(x, r)
+    assert torch.equal(g[r.pos_of_pair.long()].view(T, k, H), x[:, None].expand(T, k, H))
+    # weights sum to 1: combining copies of x gives x back, within the sum's and the output's rounding
+    ref.close(ops.combine(g, r), x.to(ref.F64), x.to(ref.F64).abs() * (k + 4) * 2.0 ** -23, "round trip")
+
+
+def test_errors_on_the_device_are_refused():
+    x, w = rnd((8, 64), BF, 63), rnd((16, 64), BF, 64)
+    with pytest.raises(ValueError, match="shape"):
+        ops.linear(x, w, rnd((15,), F, 65))
+    with pytest.raises(moe_mx.MoeMxError) as e:
+        ops.linear(x, w, out=x.view(-1)[:128].view(8, 16))
+    assert e.value.code == moe_mx.MOE_MX_ERR_INVALID_ARG and "overlap" in str(e.value)
+    with pytest.raises(moe_mx.MoeMxError, match="aligned"):
+        ops.linear(x.view(-1)[1:449].view(7, 64), w)
+    with pytest.raises(moe_mx.MoeMxError, match="workspace"):
+        moe_mx.moe_mx_linear_backward(rnd((8, 16), F, 66), x, w, None, None, None, 0, 8, 16, 64, 0, 0, 1,
+                                      torch.empty_like(x), None, None, None, 0)
