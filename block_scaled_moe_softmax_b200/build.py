@@ -20,7 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libmoe_mx.so")
 SOURCES = ["api.cu", "route_group.cu", "fc_gemm.cu", "quant.cu", "permute.cu", "linear.cu", "api_routed.cu"]
-HEADERS = ["ptx.cuh", "kernels.cuh", "host.cuh", "vec.cuh", "routed.cuh"]
+HEADERS = ["ptx.cuh", "kernels.cuh", "host.cuh", "vec.cuh", "routed.cuh", "pair.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "-I", os.path.join(ROOT, "include"),

@@ -249,6 +249,19 @@ int moe_mx_linear(const void *x, const void *w, const float *bias, const void *r
     return launched("linear launch");
 }
 
+int moe_mx_linear_status(int device, void *stream)
+{
+    clear_error();
+    int ndev = 0;
+    const cudaError_t ce = cudaGetDeviceCount(&ndev);
+    if (ce != cudaSuccess)
+        return cuda_fail(ce, "cudaGetDeviceCount");
+    if (device < 0 || device >= ndev)
+        return fail(MOE_MX_ERR_INVALID_ARG, "device %d out of range (%d devices)", device, ndev);
+    const DeviceGuard guard(device);
+    return linear_status(static_cast<cudaStream_t>(stream));
+}
+
 int moe_mx_linear_backward(const void *dout, const void *x, const void *w, const void *preact, const int32_t *counts,
                            const int32_t *pad_offsets, int num_experts, int64_t rows, int N, int K, int dtype,
                            int activation, int dout_dtype, void *dx, void *dw, float *dbias, void *workspace,

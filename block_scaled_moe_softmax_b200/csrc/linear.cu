@@ -8,6 +8,8 @@
 // dz is rounded once to the operands' type, which the products take (db sums it before that).
 #include "../../include/moe_mx.h"
 #include "host.cuh"
+#include "kernels.cuh"
+#include "pair.cuh"
 #include "routed.cuh"
 #include "vec.cuh"
 
@@ -52,11 +54,20 @@ struct Segments {
     int64_t M;
 };
 
+// Valid rows of expert e's segment, and its first row (none of a segment that starts outside the buffer).
+__device__ __forceinline__ int segment_rows(const Segments &s, int e, int &first)
+{
+    first = __ldg(s.pad_offsets + e);
+    if (first < 0 || first >= s.M)
+        return 0;
+    return max(0, min(__ldg(s.counts + e), (int)(s.M - first)));
+}
+
 // The segment holding row `r0` (a multiple of 64): its expert, and the end of its valid rows.
 __device__ __forceinline__ bool find_segment(const Segments &s, int64_t r0, int &e, int64_t &end)
 {
+    e = 0;
     if (s.E == 0) {
-        e = 0;
         end = s.M;
         return r0 < s.M;
     }
@@ -69,114 +80,10 @@ __device__ __forceinline__ bool find_segment(const Segments &s, int64_t r0, int 
             hi = mid;
     }
     e = lo;
-    const int64_t first = __ldg(s.pad_offsets + e);
-    end = min(s.M, first + __ldg(s.counts + e));
+    int first;
+    const int rows = segment_rows(s, e, first);
+    end = (int64_t)first + rows;
     return r0 >= first && r0 < end;
-}
-
-// ---------------------------------------------------------------- matrix product
-struct Gemm {
-    // D[m, n] = sum_k A[m, k] B[n, k]; element (i, k) of an operand at i * s0 + k * s1
-    const void *a, *b;
-    int64_t as0, as1, bs0, bs1;
-    int64_t b_expert; // elements from one expert's B to the next's (rows segmented)
-    int64_t d_expert; // elements from one expert's D to the next's (k segmented)
-    Segments seg;
-    int64_t M;
-    int N;
-    int64_t K;
-    int seg_k; // segments run over k (dw) instead of the rows
-    // epilogue
-    const float *bias;
-    const void *residual;
-    void *out, *preact;
-    int act, n_out; // columns of out (N / 2 for swiglu: gate columns n and up columns n + n_out)
-};
-
-constexpr int kT = 64, kTk = 16;
-
-template <typename T, typename TO> __device__ __forceinline__ void finish(const Gemm &g, int e, int64_t m, int n,
-                                                                          float z, float up)
-{
-    const float *bias = g.bias ? g.bias + (size_t)e * g.N : nullptr;
-    const bool gated = g.act == kActSwiglu;
-    if (bias) {
-        z += bias[n];
-        if (gated)
-            up += bias[n + g.n_out];
-    }
-    if (g.preact) {
-        static_cast<T *>(g.preact)[m * g.N + n] = from_f32<T>(z);
-        if (gated)
-            static_cast<T *>(g.preact)[m * g.N + n + g.n_out] = from_f32<T>(up);
-    }
-    float v = gated ? z * sigmoid(z) * up : act_fwd(z, g.act);
-    const size_t o = (size_t)e * (g.seg_k ? g.d_expert : 0) + (size_t)m * g.n_out + n;
-    if (g.residual)
-        v += to_f32<TO>(static_cast<const TO *>(g.residual)[o]);
-    static_cast<TO *>(g.out)[o] = from_f32<TO>(v);
-}
-
-// 64 x 64 tile of D, 16 of k at a time, 4 x 4 outputs a thread.
-template <typename T, typename TO> __global__ void __launch_bounds__(256) gemm_kernel(const Gemm g)
-{
-    __shared__ float sa[kTk][kT + 1], sb[kTk][kT + 1], su[kTk][kT + 1];
-    const bool gated = g.act == kActSwiglu;
-    const int64_t m0 = (int64_t)blockIdx.x * kT;
-    const int n0 = blockIdx.y * kT;
-    int e = 0;
-    int64_t m_end = g.M, k0 = 0, k_end = g.K;
-    if (g.seg_k) {
-        e = blockIdx.z;
-        if (g.seg.E) {
-            k0 = __ldg(g.seg.pad_offsets + e);
-            k_end = min(g.seg.M, k0 + __ldg(g.seg.counts + e));
-        }
-    } else if (!find_segment(g.seg, m0, e, m_end)) {
-        return;
-    }
-    const T *a = static_cast<const T *>(g.a);
-    const T *b = static_cast<const T *>(g.b) + (g.seg_k ? 0 : (size_t)e * g.b_expert);
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {}, up[4][4] = {};
-    for (int64_t k = k0; k < k_end; k += kTk) {
-        for (int i = threadIdx.x; i < kT * kTk; i += 256) {
-            // consecutive threads along the operand's unit stride
-            const int ak = g.as1 == 1 ? i % kTk : i / kT, am = g.as1 == 1 ? i / kTk : i % kT;
-            const int bk = g.bs1 == 1 ? i % kTk : i / kT, bn = g.bs1 == 1 ? i / kTk : i % kT;
-            const bool ka = k + ak < k_end, kb = k + bk < k_end, nb = n0 + bn < g.n_out;
-            sa[ak][am] = ka && m0 + am < m_end ? to_f32<T>(a[(m0 + am) * g.as0 + (k + ak) * g.as1]) : 0.f;
-            sb[bk][bn] = kb && nb ? to_f32<T>(b[(n0 + bn) * g.bs0 + (k + bk) * g.bs1]) : 0.f;
-            if (gated)
-                su[bk][bn] = kb && nb ? to_f32<T>(b[(n0 + bn + g.n_out) * g.bs0 + (k + bk) * g.bs1]) : 0.f;
-        }
-        __syncthreads();
-        for (int kk = 0; kk < kTk; ++kk)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) {
-                    acc[i][j] = fmaf(sa[kk][ty * 4 + i], sb[kk][tx * 4 + j], acc[i][j]);
-                    if (gated)
-                        up[i][j] = fmaf(sa[kk][ty * 4 + i], su[kk][tx * 4 + j], up[i][j]);
-                }
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty * 4 + i;
-            const int n = n0 + tx * 4 + j;
-            if (m < m_end && n < g.n_out)
-                finish<T, TO>(g, e, m, n, acc[i][j], up[i][j]);
-        }
-}
-
-template <typename F> void by_type(int type, F f)
-{
-    if (type == kTypeF32)
-        f(float());
-    else if (type == kTypeF16)
-        f(__half());
-    else
-        f(__nv_bfloat16());
 }
 
 template <typename F> void by_half(int type, F f)
@@ -187,17 +94,628 @@ template <typename F> void by_half(int type, F f)
         f(__nv_bfloat16());
 }
 
-void launch_gemm(const Gemm &g, int type, int out_type, cudaStream_t s)
+// ---------------------------------------------------------------- matrix product
+// D[m, n] = sum_k A[m, k] B[n, k] on tcgen05, two CTAs to a 256 x BN tile (cta_group::2): each holds
+// 128 rows of A and half of B's rows in shared memory and 128 rows of the accumulator in its TMEM.
+// Warp 0 copies 64-deep k blocks in with TMA, warp 1 of the leader issues the MMAs, warps 4..11 take
+// a finished accumulator out while the next tile's runs in the other half of TMEM.
+//
+// Operands with k contiguous (x and w of the forward pass, dz in dx) are K-major tiles; those with
+// k along the rows (w in dx; dz and x in dw) are read as they lie, as M- or N-major tiles.
+struct Gemm {
+    Segments seg;
+    int seg_k;            // the segments run over k (dw) instead of the rows
+    int M, n_cols, K;     // rows and columns of D, depth (dense, or of a rows-segmented product)
+    int kb_split;         // k blocks of one split (dense only), split s writes plane s of out
+    int mt, nt, splits;   // tiles of a dense product, or of one expert's when the segments run over k
+    int gated;            // swiglu: the pair's CTAs take the gate and the up rows of B
+    int fmt;              // 0: f16, 1: bf16
+    // epilogue
+    const float *bias;
+    const void *residual;
+    void *out, *preact;
+    int act, N;           // columns of preact, and of each expert's bias
+    int type, out_type, vec;
+    int64_t d_expert;     // elements from one expert's D to the next's (seg_k)
+};
+
+constexpr int kTileM = 256, kBk = 64, kMaxSeg = kMaxExperts;
+constexpr int kThreads = 384, kEpiWarps = 8;
+constexpr unsigned long long kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
+
+template <int BN> struct Cfg {
+    static constexpr int kABytes = 128 * kBk * 2, kBBytes = BN / 2 * kBk * 2, kStage = kABytes + kBBytes;
+    static constexpr int kStages = BN == 256 ? 5 : BN == 192 ? 6 : 7;
+    static constexpr int kOffEpi = kStages * kStage, kOffBar = kOffEpi + kEpiWarps * 4096;
+    // barriers: full, empty, tail per stage, 2 acc_full, 2 acc_empty, mma_done; then the TMEM address
+    static constexpr int kNumBar = 3 * kStages + 5;
+    static constexpr int kOffPrefix = kOffBar + kNumBar * 8 + 8;
+    static constexpr int kSmem = kOffPrefix + (kMaxSeg + 1) * 4 + 1024; // + alignment of the base
+};
+
+struct Tile {
+    int e, row, row_end; // first row of D, and the end of the rows that are stored
+    int n0;              // first column of D
+    int k0, nkb, rem;    // first k (element), k blocks, valid rows of the last (0: all)
+    int split;
+};
+
+// The t-th tile.  Rows-segmented: prefix[e] holds the number of tiles of the experts before e, tiles run
+// over an expert's row tiles first, so that neighbouring pairs read the same rows of B.
+template <int BN> __device__ __forceinline__ bool get_tile(const Gemm &g, const int32_t *prefix, int t, Tile &o)
 {
-    const dim3 grid((unsigned)((g.M + kT - 1) / kT), (g.n_out + kT - 1) / kT,
-                    g.seg_k && g.seg.E ? g.seg.E : 1);
-    by_half(type, [&](auto x) {
-        using T = decltype(x);
-        if (out_type == kTypeF32)
-            gemm_kernel<T, float><<<grid, 256, 0, s>>>(g);
+    const int bn = g.gated ? BN / 2 : BN;
+    o.rem = 0, o.split = 0;
+    if (g.seg.E == 0) {
+        const int per = g.mt * g.nt;
+        o.split = t / per;
+        if (o.split >= g.splits)
+            return false;
+        t -= o.split * per;
+        o.e = 0, o.row = t % g.mt * kTileM, o.row_end = g.M, o.n0 = t / g.mt * bn;
+        const int kb = (g.K + kBk - 1) / kBk, lo = o.split * g.kb_split;
+        o.k0 = lo * kBk, o.nkb = min(g.kb_split, kb - lo);
+        return true;
+    }
+    if (g.seg_k) {
+        const int per = g.mt * g.nt;
+        o.e = t / per;
+        if (o.e >= g.seg.E)
+            return false;
+        t -= o.e * per;
+        o.row = t % g.mt * kTileM, o.row_end = g.M, o.n0 = t / g.mt * bn;
+        int first;
+        const int rows = segment_rows(g.seg, o.e, first);
+        o.k0 = first, o.nkb = (rows + kBk - 1) / kBk, o.rem = rows % kBk;
+        return true;
+    }
+    if (t >= prefix[g.seg.E])
+        return false;
+    int lo = 0, hi = g.seg.E; // the last e with prefix[e] <= t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (prefix[mid] <= t)
+            lo = mid;
         else
-            gemm_kernel<T, T><<<grid, 256, 0, s>>>(g);
-    });
+            hi = mid;
+    }
+    int first;
+    const int rows = segment_rows(g.seg, lo, first);
+    const int mt = (rows + kTileM - 1) / kTileM;
+    t -= prefix[lo];
+    o.e = lo, o.row = first + t % mt * kTileM, o.row_end = first + rows, o.n0 = t / mt * bn;
+    o.k0 = 0, o.nkb = (g.K + kBk - 1) / kBk;
+    return true;
+}
+
+// Eight neighbouring values of one row of D: bias, preact, activation, residual, store.
+__device__ __forceinline__ void load8(const void *p, int type, size_t o, float (&f)[8])
+{
+    if (type == kTypeF32) {
+        Raw<float, 8> r;
+        r.load(static_cast<const float *>(p) + o);
+        r.get(f);
+    } else if (type == kTypeF16) {
+        Raw<__half, 8> r;
+        r.load(static_cast<const __half *>(p) + o);
+        r.get(f);
+    } else {
+        Raw<__nv_bfloat16, 8> r;
+        r.load(static_cast<const __nv_bfloat16 *>(p) + o);
+        r.get(f);
+    }
+}
+__device__ __forceinline__ void store8(void *p, int type, size_t o, const float (&f)[8])
+{
+    if (type == kTypeF32)
+        Raw<float, 8>::put(static_cast<float *>(p) + o, f);
+    else if (type == kTypeF16)
+        Raw<__half, 8>::put(static_cast<__half *>(p) + o, f);
+    else
+        Raw<__nv_bfloat16, 8>::put(static_cast<__nv_bfloat16 *>(p) + o, f);
+}
+__device__ __forceinline__ float load1(const void *p, int type, size_t o)
+{
+    return type == kTypeF32   ? static_cast<const float *>(p)[o]
+           : type == kTypeF16 ? __half2float(static_cast<const __half *>(p)[o])
+                              : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[o]);
+}
+__device__ __forceinline__ void store1(void *p, int type, size_t o, float v)
+{
+    if (type == kTypeF32)
+        static_cast<float *>(p)[o] = v;
+    else if (type == kTypeF16)
+        static_cast<__half *>(p)[o] = __float2half_rn(v);
+    else
+        static_cast<__nv_bfloat16 *>(p)[o] = __float2bfloat16_rn(v);
+}
+
+// What the epilogue of a product needs (shared by the kernels).
+struct Epi {
+    const float *bias;    // of this expert, or nullptr
+    const void *residual;
+    void *out, *preact;
+    int act, N, n_cols, type, out_type, vec;
+};
+
+// z (and up for swiglu): 8 columns of row m from column n.
+__device__ __forceinline__ void finish8(const Epi &g, int64_t m, int n, float (&z)[8], float (&up)[8],
+                                        const float (&bz)[8], const float (&bu)[8], size_t d_off)
+{
+    const bool gated = g.act == kActSwiglu;
+    if (g.bias) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            z[i] += bz[i];
+            if (gated)
+                up[i] += bu[i];
+        }
+    }
+    const size_t o = d_off + (size_t)m * g.n_cols + n, po = (size_t)m * g.N + n;
+    if (g.vec) {
+        if (g.preact) {
+            store8(g.preact, g.type, po, z);
+            if (gated)
+                store8(g.preact, g.type, po + g.n_cols, up);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] = gated ? z[i] * sigmoid(z[i]) * up[i] : act_fwd(z[i], g.act);
+        if (g.residual) {
+            float r[8];
+            load8(g.residual, g.out_type, o, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                z[i] += r[i];
+        }
+        store8(g.out, g.out_type, o, z);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (n + i >= g.n_cols)
+            break;
+        if (g.preact) {
+            store1(g.preact, g.type, po + i, z[i]);
+            if (gated)
+                store1(g.preact, g.type, po + g.n_cols + i, up[i]);
+        }
+        float v = gated ? z[i] * sigmoid(z[i]) * up[i] : act_fwd(z[i], g.act);
+        if (g.residual)
+            v += load1(g.residual, g.out_type, o + i);
+        store1(g.out, g.out_type, o + i, v);
+    }
+}
+
+__device__ __forceinline__ void load_bias8(const Epi &g, int n, float (&bz)[8], float (&bu)[8])
+{
+    if (!g.bias)
+        return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const bool in = n + i < g.n_cols;
+        bz[i] = in ? __ldg(g.bias + n + i) : 0.f;
+        bu[i] = in && g.act == kActSwiglu ? __ldg(g.bias + n + i + g.n_cols) : 0.f;
+    }
+}
+
+__device__ uint32_t g_linear_err; // set by a wait that gave up
+
+template <int BN, bool kAMn, bool kBMn>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    gemm_kernel(const Gemm g, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b)
+{
+    using C = Cfg<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *const sm = smem_raw + (base - smem_u32(smem_raw));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    constexpr int S = C::kStages;
+    const uint32_t bar0 = base + C::kOffBar;
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (S + s); };
+    auto tail = [&](int s) { return bar0 + 8u * (2 * S + s); };
+    auto acc_full = [&](int b) { return bar0 + 8u * (3 * S + b); };
+    auto acc_empty = [&](int b) { return bar0 + 8u * (3 * S + 2 + b); };
+    const uint32_t mma_done = bar0 + 8u * (3 * S + 4), tmem_slot = bar0 + 8u * C::kNumBar;
+    int32_t *const prefix = reinterpret_cast<int32_t *>(sm + C::kOffPrefix);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full(s), 2);  // each CTA's copies (or its tail warp)
+            mbar_init(empty(s), 1); // the commit of the MMAs that read the stage
+            mbar_init(tail(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(acc_full(b), 1);
+            mbar_init(acc_empty(b), 2 * kEpiWarps);
+        }
+        mbar_init(mma_done, 1);
+        fence_mbar_init();
+        prefetch_tensormap(&map_a);
+        prefetch_tensormap(&map_b);
+    }
+    if (warp == 2)
+        tmem_alloc_pair(tmem_slot, 512);
+    grid_dep_wait(); // everything this kernel reads, and the buffers it writes
+    grid_dep_launch();
+    if (warp == 3 && g.seg.E && !g.seg_k) {
+        int run = 0;
+        for (int e0 = 0; e0 < g.seg.E; e0 += 32) {
+            const int e = e0 + lane;
+            int n = 0;
+            if (e < g.seg.E) {
+                int first;
+                const int rows = segment_rows(g.seg, e, first);
+                n = (rows + kTileM - 1) / kTileM * g.nt;
+            }
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                if (lane >= o)
+                    incl += y;
+            }
+            if (e < g.seg.E)
+                prefix[e] = run + incl - n;
+            run += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        }
+        if (lane == 0)
+            prefix[g.seg.E] = run;
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync(); // barriers of both CTAs are set up
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + C::kOffBar + 8 * C::kNumBar);
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    Tile t;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ copies
+        uint32_t it = 0; // k blocks issued
+        bool ok = true;
+        for (int i = pair; ok && get_tile<BN>(g, prefix, i, t); i += pairs) {
+            const int a_row = t.row + (int)rank * 128;
+            const int b_row = g.gated ? (int)rank * g.n_cols + t.n0 : t.n0 + (int)rank * (BN / 2);
+            for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+                const int s = it % S;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(empty(s), ((it / S) & 1) ^ 1, &g_linear_err, kWaitNs))) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    const int k = t.k0 + kb * kBk;
+                    // the last block of a segment inside the rows: this CTA's tail warp clears the rows
+                    // behind the segment before the leader may use the block
+                    const bool cut = t.rem && kb == t.nkb - 1;
+                    uint32_t bar = map_rank(full(s), 0);
+                    if (cut) {
+                        bar = map_rank(tail(s), rank);
+                        mbar_arrive_expect_tx(tail(s), C::kStage);
+                    } else {
+                        mbar_arrive_expect_tx_cluster(bar, C::kStage);
+                    }
+                    const uint32_t sa = base + s * C::kStage, sb = sa + C::kABytes;
+                    if (kAMn) {
+                        for (int j = 0; j < 2; ++j)
+                            tma_pair_2d(sa + j * 8192, &map_a, a_row + j * 64, k, bar);
+                    } else {
+                        tma_pair_2d(sa, &map_a, k, a_row, bar);
+                    }
+                    if (kBMn) {
+                        for (int j = 0; j < BN / 128; ++j)
+                            tma_pair_3d(sb + j * 8192, &map_b, b_row + j * 64, k, g.seg_k ? 0 : t.e, bar);
+                    } else {
+                        tma_pair_3d(sb, &map_b, k, b_row, t.e, bar);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        // Before either CTA may exit, every copy has landed (all report to the leader's barriers; a wait
+        // that gave up leaves some unread) and every commit has reached this CTA's barriers.
+        for (int j = 0; j < S; ++j)
+            if (it > (uint32_t)j) {
+                const uint32_t last = it - 1 - j;
+                if (rank == 0)
+                    mbar_wait_cluster(full(last % S), (last / S) & 1, nullptr, kDrainNs);
+                mbar_wait_cluster(empty(last % S), (last / S) & 1, nullptr, kDrainNs);
+            }
+    } else if (warp == 1 && rank == 1) {
+        mbar_wait_cluster(mma_done, 0, nullptr, kDrainNs); // the leader's last commit
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMAs
+        const uint32_t idesc = idesc_f16(g.fmt, kAMn, kBMn, kTileM, BN);
+        uint32_t it = 0, n = 0;
+        bool ok = true;
+        for (int i = pair; ok && get_tile<BN>(g, prefix, i, t); i += pairs) {
+            if (t.nkb == 0)
+                continue;
+            const int buf = n & 1;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(acc_empty(buf), ((n >> 1) & 1) ^ 1, &g_linear_err, kWaitNs)))
+                break;
+            ++n;
+            tc_fence_after();
+            for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+                const int s = it % S;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(full(s), (it / S) & 1, &g_linear_err, kWaitNs))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (elect_lane()) {
+                    const uint32_t sa = base + s * C::kStage, sb = sa + C::kABytes;
+                    const uint64_t da = kAMn ? smem_desc_mn_sw128(sa, 8192) : smem_desc_sw128(sa);
+                    const uint64_t db = kBMn ? smem_desc_mn_sw128(sb, 8192) : smem_desc_sw128(sb);
+                    // 16 of k: 32 bytes of a K-major row, or two 1024-byte groups of 8 k
+#pragma unroll
+                    for (int q = 0; q < kBk / 16; ++q)
+                        umma_f16_pair(tmem + 256u * buf, da + q * (kAMn ? 128 : 2), db + q * (kBMn ? 128 : 2), idesc,
+                                      kb > 0 || q > 0);
+                    umma_commit_pair(empty(s));
+                    if (kb == t.nkb - 1)
+                        umma_commit_pair(acc_full(buf));
+                }
+                __syncwarp();
+            }
+        }
+        // every MMA has completed before TMEM is released
+        if (elect_lane())
+            umma_commit_pair(mma_done);
+        __syncwarp();
+        mbar_wait_cluster(mma_done, 0, nullptr, kDrainNs);
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ cut k blocks
+        if (kAMn && kBMn && g.seg.E) {
+            uint32_t it = 0, ph = 0; // ph: the phase of each stage's tail barrier
+            bool ok = true;
+            for (int i = pair; ok && get_tile<BN>(g, prefix, i, t); i += pairs) {
+                it += t.nkb;
+                if (!t.rem)
+                    continue;
+                const int s = (it - 1) % S;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(tail(s), (ph >> s) & 1, &g_linear_err, kWaitNs))) {
+                    ok = false;
+                    break;
+                }
+                ph ^= 1u << s;
+                // rows (of k) behind the segment, in each box of 64 rows x 128 bytes
+                uint8_t *const st = sm + s * C::kStage;
+                for (int b = 0; b < C::kStage / 8192; ++b)
+                    for (int r = t.rem * 8 + lane; r < 64 * 8; r += 32)
+                        reinterpret_cast<uint4 *>(st + b * 8192)[r] = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(map_rank(full(s), 0));
+                __syncwarp();
+            }
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        float *const stg = reinterpret_cast<float *>(sm + C::kOffEpi + (warp - 4) * 4096);
+        const int cols = g.gated ? BN / 4 : BN / 2; // columns of D this warp takes
+        const int rl = lane >> 2, c8 = (lane & 3) * 8;
+        uint32_t n = 0;
+        // accumulator columns [c, c + 32) of this warp's 32 rows, through shared memory: lane l then
+        // holds row 8 it + l / 4, columns 8 (l % 4) .. + 7
+        auto chunk = [&](uint32_t c, float (&v)[4][8]) {
+            uint32_t r0[16], r1[16];
+            tmem_ld16(c, r0);
+            tmem_ld16(c + 16, r1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float4 *row = reinterpret_cast<float4 *>(stg + lane * 32);
+                row[j ^ (lane & 7)] = make_float4(__uint_as_float(r0[4 * j]), __uint_as_float(r0[4 * j + 1]),
+                                                  __uint_as_float(r0[4 * j + 2]), __uint_as_float(r0[4 * j + 3]));
+                row[(j + 4) ^ (lane & 7)] = make_float4(__uint_as_float(r1[4 * j]), __uint_as_float(r1[4 * j + 1]),
+                                                        __uint_as_float(r1[4 * j + 2]), __uint_as_float(r1[4 * j + 3]));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = i * 8 + rl;
+                const float4 *row = reinterpret_cast<const float4 *>(stg + r * 32);
+                const float4 a = row[(c8 / 4) ^ (r & 7)], b = row[(c8 / 4 + 1) ^ (r & 7)];
+                v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
+                v[i][4] = b.x, v[i][5] = b.y, v[i][6] = b.z, v[i][7] = b.w;
+            }
+            __syncwarp();
+        };
+        for (int i = pair; get_tile<BN>(g, prefix, i, t); i += pairs) {
+            const int buf = n & 1;
+            if (t.nkb > 0) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(acc_full(buf), (n >> 1) & 1, &g_linear_err, kWaitNs)))
+                    break;
+                ++n;
+                tc_fence_after();
+            }
+            Epi ep{g.bias ? g.bias + (size_t)t.e * g.N : nullptr, g.residual, g.out, g.preact, g.act, g.N, g.n_cols,
+                   g.type, g.out_type, g.vec};
+            const size_t d_off = g.seg_k ? (size_t)t.e * g.d_expert : (size_t)t.split * g.M * g.n_cols;
+            const uint32_t acc = tmem + 256u * buf + ((uint32_t)(q * 32) << 16);
+            for (int c = 0; c < cols; c += 32) {
+                const int lc = half * cols + c; // column within the tile
+                float v[4][8] = {}, up[4][8] = {}, bz[8], bu[8];
+                const int nn = t.n0 + lc + c8;
+                load_bias8(ep, nn, bz, bu);
+                if (t.nkb > 0) {
+                    chunk(acc + lc, v);
+                    if (g.gated)
+                        chunk(acc + BN / 2 + lc, up);
+                }
+                if (nn < g.n_cols)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int64_t m = (int64_t)t.row + (int)rank * 128 + q * 32 + j * 8 + rl;
+                        if (m < t.row_end)
+                            finish8(ep, m, nn, v[j], up[j], bz, bu, d_off);
+                    }
+            }
+            if (t.nkb > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(map_rank(acc_empty(buf), 0));
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 2) {
+        tmem_relinquish_pair();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- split products
+// out = epilogue(sum over the splits' float32 planes, in order); one thread per 8 columns of a row.
+__global__ void __launch_bounds__(256) reduce_kernel(const float *__restrict__ planes, int splits, int M, Epi g)
+{
+    grid_dep_wait();
+    grid_dep_launch();
+    const int per_row = (g.n_cols + 7) / 8;
+    const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+    if (i >= (int64_t)M * per_row)
+        return;
+    const int64_t m = i / per_row;
+    const int n = (int)(i % per_row) * 8;
+    const bool gated = g.act == kActSwiglu;
+    const size_t plane = (size_t)M * g.N;
+    float z[8] = {}, up[8] = {}, bz[8], bu[8];
+    load_bias8(g, n, bz, bu);
+    for (int s = 0; s < splits; ++s) {
+        const float *p = planes + s * plane + m * g.N + n;
+        if (g.vec) {
+            float f[8];
+            load8(p, kTypeF32, 0, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                z[j] += f[j];
+            if (gated) {
+                load8(p, kTypeF32, g.n_cols, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    up[j] += f[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (n + j < g.n_cols) {
+                    z[j] += p[j];
+                    if (gated)
+                        up[j] += p[j + g.n_cols];
+                }
+        }
+    }
+    finish8(g, m, n, z, up, bz, bu, 0);
+}
+
+// ---------------------------------------------------------------- unaligned rows
+// TMA reads rows that start on 16 bytes: operands whose row length is not a multiple of 8 are first
+// copied to rows of the next multiple (the pad is not read: the tensor map ends at the true length).
+__global__ void __launch_bounds__(256) pack_kernel(const uint16_t *__restrict__ src, uint16_t *__restrict__ dst,
+                                                   int64_t rows, int cols, int ld)
+{
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int c = threadIdx.x; c < cols; c += blockDim.x)
+            dst[r * ld + c] = src[r * cols + c];
+}
+
+void launch_pack(const void *src, void *dst, int64_t rows, int cols, cudaStream_t s)
+{
+    const int64_t want = rows < 65536 ? rows : 65536;
+    pack_kernel<<<(unsigned)(want > 0 ? want : 1), 256, 0, s>>>(static_cast<const uint16_t *>(src),
+                                                                 static_cast<uint16_t *>(dst), rows, cols,
+                                                                 (int)round_up(cols, 8));
+}
+
+// ---------------------------------------------------------------- launch
+constexpr int kPairs = 74; // SM pairs of the 148-SM part the plans are made for
+
+// Tile width and splits of a dense [M, cols] product over kb blocks of k, by the estimated cycles:
+// a 64-deep block of a 256 x BN tile takes about 256 + BN cycles (its MMAs 2 BN, its loads from L2
+// (16 KB + 64 BN bytes) / 64 a cycle), a tile about 1500 to start and finish, and a split product
+// writes and reads its float32 planes and launches a second kernel.
+struct Plan {
+    int bn, splits;
+};
+Plan plan_dense(int64_t M, int cols, int kb, bool gated, bool mn)
+{
+    Plan best{256, 1};
+    if (kb == 0)
+        return best;
+    double best_t = 1e30;
+    const int64_t mt = (M + kTileM - 1) / kTileM;
+    for (int bn : {256, 192, 128}) {
+        if (bn == 192 && (gated || mn)) // halves of 96 columns
+            continue;
+        for (int s = 1; s <= 16; ++s) {
+            if (s > 1 && kb / s < 4)
+                break;
+            const int64_t kbs = (kb + s - 1) / s;
+            const int64_t tiles = mt * ((cols + bn - 1) / bn) * ((kb + kbs - 1) / kbs);
+            double t = (double)((tiles + kPairs - 1) / kPairs) * ((double)kbs * (256 + bn) + 1500);
+            if (s > 1)
+                t += 5000 + (double)s * M * cols * 8 / 4000;
+            if (t < best_t)
+                best_t = t, best = Plan{bn, s};
+        }
+    }
+    return best;
+}
+
+template <int BN, bool kAMn, bool kBMn>
+int launch_gemm(const Gemm &g, const CUtensorMap &ma, const CUtensorMap &mb, int tiles, cudaStream_t s)
+{
+    auto kernel = gemm_kernel<BN, kAMn, kBMn>;
+    // per device and cheap; nothing to remember between calls
+    cudaError_t ce = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::kSmem);
+    if (ce != cudaSuccess)
+        return cuda_fail(ce, "cudaFuncSetAttribute(linear)");
+    const int pairs = tiles < kPairs ? tiles : kPairs;
+    ce = launch_kernel(kernel, dim3(2 * pairs), dim3(kThreads), Cfg<BN>::kSmem, s, true, g, ma, mb);
+    return ce == cudaSuccess ? MOE_MX_OK : cuda_fail(ce, "linear product launch");
+}
+
+// A product's operands as the kernel reads them: pointer, contiguous extent, rows, elements per row.
+struct Operand {
+    const void *p;
+    int64_t inner, rows, ld;
+    int experts; // planes of rows (B of a rows-segmented product), else 1
+};
+
+int make_map(CUtensorMap *map, const Operand &o, int box_rows, bool three)
+{
+    const cuuint64_t dims[3] = {(cuuint64_t)o.inner, (cuuint64_t)o.rows, (cuuint64_t)o.experts};
+    const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, (cuuint64_t)o.ld * 2 * o.rows};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+    return encode_nd(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, three ? 3 : 2, o.p, dims, strides, box);
+}
+
+// tiles: an upper bound of the product's tiles (the kernel finds a grouped product's on the device)
+template <bool kAMn, bool kBMn>
+int run_gemm(Gemm &g, int bn, const Operand &a, const Operand &b, int64_t tiles, cudaStream_t s)
+{
+    if (tiles > INT32_MAX)
+        return fail(MOE_MX_ERR_UNSUPPORTED, "the product has %lld tiles", (long long)tiles);
+    CUtensorMap ma, mb;
+    int rc;
+    if ((rc = make_map(&ma, a, kAMn ? 64 : 128, false)) || (rc = make_map(&mb, b, kBMn ? 64 : bn / 2, true)))
+        return rc;
+    if (bn == 256)
+        return launch_gemm<256, kAMn, kBMn>(g, ma, mb, (int)tiles, s);
+    if constexpr (!kBMn)
+        if (bn == 192)
+            return launch_gemm<192, kAMn, kBMn>(g, ma, mb, (int)tiles, s);
+    return launch_gemm<128, kAMn, kBMn>(g, ma, mb, (int)tiles, s);
 }
 
 // ---------------------------------------------------------------- dz and the bias gradient
@@ -291,9 +809,9 @@ __global__ void __launch_bounds__(256) dbias_kernel(const float *part, Segments 
         return;
     int64_t b0 = 0, rows = seg.M;
     if (seg.E) {
-        const int64_t first = __ldg(seg.pad_offsets + e);
+        int first;
+        rows = segment_rows(seg, e, first);
         b0 = first / 128;
-        rows = min((int64_t)__ldg(seg.counts + e), seg.M - first);
     }
     float t = 0.f;
     for (int64_t b = 0; b * 128 < rows; ++b)
@@ -305,41 +823,149 @@ int ldz_of(int N) { return (int)round_up(N, 8); }
 
 bool dz_is_dout(int act, int type, int dout_type, int N) { return act == kActNone && type == dout_type && N % 8 == 0; }
 
+
+// Workspace parts of a call, in order; an absent part has no bytes.
+struct Parts {
+    int64_t at = 0;
+    int64_t take(int64_t bytes)
+    {
+        const int64_t o = at;
+        at += round_up(bytes, 256);
+        return o;
+    }
+};
+
+struct ForwardPlan {
+    Plan p;
+    int64_t x, w, planes, bytes;
+};
+ForwardPlan plan_linear(int E, int64_t M, int N, int K, int act)
+{
+    ForwardPlan f{};
+    const bool gated = act == kActSwiglu;
+    const int kb = (K + kBk - 1) / kBk;
+    if (E == 0) {
+        // a gated product is one of N columns in tiles of the gate's and the up's; a split one is plain
+        f.p = plan_dense(M, N, kb, gated, false);
+    } else {
+        f.p = Plan{N > 128 ? 256 : 128, 1};
+    }
+    Parts ws;
+    f.x = ws.take(K % 8 ? M * round_up(K, 8) * 2 : 0);
+    f.w = ws.take(K % 8 ? (E ? E : 1) * (int64_t)N * round_up(K, 8) * 2 : 0);
+    f.planes = ws.take(f.p.splits > 1 ? f.p.splits * M * N * 4 : 0);
+    f.bytes = ws.at;
+    return f;
+}
+
+struct BackwardPlan {
+    bool direct;
+    Plan dw;
+    int64_t part, dz, x, w, planes, bytes;
+};
+BackwardPlan plan_backward(int E, int64_t M, int N, int K, int act, int type, int dout_type)
+{
+    BackwardPlan f{};
+    f.direct = dz_is_dout(act, type, dout_type, N);
+    f.dw = Plan{256, 1};
+    if (E == 0)
+        f.dw = plan_dense(N, K, (int)((M + kBk - 1) / kBk), false, true);
+    Parts ws;
+    f.part = ws.take((M + 127) / 128 * N * 4);
+    f.dz = ws.take(f.direct ? 0 : M * ldz_of(N) * 2);
+    f.x = ws.take(K % 8 ? M * round_up(K, 8) * 2 : 0);
+    f.w = ws.take(K % 8 ? (E ? E : 1) * (int64_t)N * round_up(K, 8) * 2 : 0);
+    f.planes = ws.take(f.dw.splits > 1 ? (int64_t)f.dw.splits * N * K * 4 : 0);
+    f.bytes = ws.at;
+    return f;
+}
+
+const void *packed(const void *p, int64_t rows, int cols, char *ws, int64_t at, cudaStream_t s)
+{
+    if (cols % 8 == 0)
+        return p;
+    launch_pack(p, ws + at, rows, cols, s);
+    return ws + at;
+}
+
+// The sum of a split product's planes, through the epilogue.
+int launch_reduce(const float *planes, int splits, int64_t M, const Epi &e, cudaStream_t s)
+{
+    const int64_t n = M * ((e.n_cols + 7) / 8);
+    const cudaError_t ce = launch_kernel(reduce_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, true, planes,
+                                         splits, (int)M, e);
+    return ce == cudaSuccess ? MOE_MX_OK : cuda_fail(ce, "split sum launch");
+}
+
+Epi epilogue_of(const Gemm &g)
+{
+    return Epi{g.bias, g.residual, g.out, g.preact, g.act, g.N, g.n_cols, g.type, g.out_type, g.vec};
+}
+
+// Turn a dense product into one that writes its splits' float32 planes.
+void split_out(Gemm &g, int splits, int kb, int N, void *planes)
+{
+    g.splits = splits;
+    g.kb_split = (kb + splits - 1) / splits;
+    g.splits = (kb + g.kb_split - 1) / g.kb_split;
+    if (splits == 1)
+        return;
+    g.gated = 0, g.n_cols = N, g.act = kActNone;
+    g.bias = nullptr, g.residual = nullptr, g.preact = nullptr;
+    g.out = planes, g.out_type = kTypeF32;
+}
+
 } // namespace
 
-int64_t linear_workspace(int, int64_t, int, int, int, int, int) { return 0; }
-
-int64_t linear_backward_workspace(int, int64_t M, int N, int, int act, int type, int dout_type)
+int64_t linear_workspace(int E, int64_t M, int N, int K, int act, int, int)
 {
-    int64_t b = round_up((M + 127) / 128 * N * 4, 256);
-    if (!dz_is_dout(act, type, dout_type, N))
-        b += round_up(M * ldz_of(N) * 2, 256);
-    return b;
+    return plan_linear(E, M, N, K, act).bytes;
+}
+
+int64_t linear_backward_workspace(int E, int64_t M, int N, int K, int act, int type, int dout_type)
+{
+    return plan_backward(E, M, N, K, act, type, dout_type).bytes;
 }
 
 int launch_linear(const LinearArgs &a, cudaStream_t s)
 {
+    const ForwardPlan f = plan_linear(a.E, a.M, a.N, a.K, a.act);
+    char *ws = static_cast<char *>(a.ws);
+    const int ld = (int)round_up(a.K, 8), experts = a.E ? a.E : 1;
+    const Operand x{packed(a.x, a.M, a.K, ws, f.x, s), a.K, a.M, ld, 1};
+    const Operand w{packed(a.w, (int64_t)experts * a.N, a.K, ws, f.w, s), a.K, a.N, ld, experts};
     Gemm g{};
-    g.a = a.x, g.as0 = a.K, g.as1 = 1;
-    g.b = a.w, g.bs0 = a.K, g.bs1 = 1, g.b_expert = (int64_t)a.N * a.K;
     g.seg = Segments{a.counts, a.pad_offsets, a.E, a.M};
-    g.M = a.M, g.N = a.N, g.K = a.K, g.n_out = a.No();
-    g.bias = a.bias, g.residual = a.residual, g.out = a.out, g.preact = a.preact, g.act = a.act;
-    launch_gemm(g, a.type, a.out_type, s);
-    return MOE_MX_OK;
+    g.M = (int)a.M, g.n_cols = a.No(), g.N = a.N, g.K = a.K;
+    g.gated = a.act == kActSwiglu, g.act = a.act, g.fmt = a.type == kTypeBf16;
+    g.bias = a.bias, g.residual = a.residual, g.out = a.out, g.preact = a.preact;
+    g.type = a.type, g.out_type = a.out_type, g.vec = g.n_cols % 8 == 0;
+    const Epi ep = epilogue_of(g);
+    const int kb = (a.K + kBk - 1) / kBk;
+    split_out(g, f.p.splits, kb, a.N, ws + f.planes);
+    const int bn = g.gated ? f.p.bn / 2 : f.p.bn;
+    g.nt = (g.n_cols + bn - 1) / bn;
+    g.mt = (int)((a.M + kTileM - 1) / kTileM);
+    // grouped: every expert hit has at most one part-filled row tile
+    const int64_t mt = a.E ? a.M / kTileM + a.E : g.mt;
+    const int rc = run_gemm<false, false>(g, f.p.bn, x, w, mt * g.nt * g.splits, s);
+    if (rc || g.splits == 1)
+        return rc;
+    return launch_reduce(reinterpret_cast<float *>(ws + f.planes), g.splits, a.M, ep, s);
 }
 
 int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
 {
     const Segments seg{a.counts, a.pad_offsets, a.E, a.M};
-    const bool direct = dz_is_dout(a.act, a.type, a.dout_type, a.N);
-    float *part = static_cast<float *>(a.ws);
+    const BackwardPlan f = plan_backward(a.E, a.M, a.N, a.K, a.act, a.type, a.dout_type);
+    char *ws = static_cast<char *>(a.ws);
+    float *part = reinterpret_cast<float *>(ws + f.part);
     DzArgs d{};
     d.dout = a.dout, d.preact = a.preact, d.seg = seg;
     d.N = a.N, d.n_out = a.No(), d.ldz = ldz_of(a.N), d.act = a.act;
     d.part = a.dbias ? part : nullptr;
-    if (!direct && (a.dx || a.dw))
-        d.dz = static_cast<char *>(a.ws) + round_up((a.M + 127) / 128 * a.N * 4, 256);
+    if (!f.direct && (a.dx || a.dw))
+        d.dz = ws + f.dz;
     if (a.M > 0 && (d.part || d.dz)) {
         const dim3 grid((unsigned)((a.M + 127) / 128), (d.n_out + 63) / 64);
         by_half(a.type, [&](auto x) {
@@ -361,24 +987,62 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
         const dim3 grid((a.N + 255) / 256, a.E ? a.E : 1);
         dbias_kernel<<<grid, 256, 0, s>>>(part, seg, a.N, a.dbias);
     }
-    const void *dz = direct ? a.dout : d.dz;
-    const int ldz = direct ? a.N : d.ldz;
+    const void *dz = f.direct ? a.dout : d.dz;
+    const int ldz = f.direct ? a.N : d.ldz, ldk = (int)round_up(a.K, 8), experts = a.E ? a.E : 1;
+    int rc;
     if (a.dx && a.M > 0) {
+        const Operand oa{dz, a.N, a.M, ldz, 1};
+        const Operand ob{packed(a.w, (int64_t)experts * a.N, a.K, ws, f.w, s), a.K, a.N, ldk, experts};
         Gemm g{};
-        g.a = dz, g.as0 = ldz, g.as1 = 1;
-        g.b = a.w, g.bs0 = 1, g.bs1 = a.K, g.b_expert = (int64_t)a.N * a.K;
-        g.seg = seg, g.M = a.M, g.N = g.n_out = a.K, g.K = a.N, g.out = a.dx;
-        launch_gemm(g, a.type, a.type, s);
+        g.seg = seg, g.M = (int)a.M, g.n_cols = g.N = a.K, g.K = a.N;
+        g.fmt = a.type == kTypeBf16, g.out = a.dx, g.type = g.out_type = a.type, g.vec = a.K % 8 == 0;
+        const int kb = (a.N + kBk - 1) / kBk;
+        const int bn = a.K > 128 ? 256 : 128;
+        split_out(g, 1, kb, a.K, nullptr);
+        g.nt = (a.K + bn - 1) / bn;
+        g.mt = (int)((a.M + kTileM - 1) / kTileM);
+        const int64_t mt = a.E ? a.M / kTileM + a.E : g.mt;
+        if ((rc = run_gemm<false, true>(g, bn, oa, ob, mt * g.nt, s)))
+            return rc;
     }
     if (a.dw) {
+        if (a.M == 0) { // no rows: zeros
+            const cudaError_t ce = cudaMemsetAsync(a.dw, 0, (size_t)experts * a.N * a.K * 2, s);
+            return ce == cudaSuccess ? MOE_MX_OK : cuda_fail(ce, "cudaMemsetAsync(dw)");
+        }
+        const Operand oa{dz, a.N, a.M, ldz, 1};
+        const Operand ob{packed(a.x, a.M, a.K, ws, f.x, s), a.K, a.M, ldk, 1};
         Gemm g{};
-        g.a = dz, g.as0 = 1, g.as1 = ldz;
-        g.b = a.x, g.bs0 = 1, g.bs1 = a.K;
-        g.seg = seg, g.seg_k = 1, g.d_expert = (int64_t)a.N * a.K;
-        g.M = a.N, g.N = g.n_out = a.K, g.K = a.M, g.out = a.dw;
-        launch_gemm(g, a.type, a.type, s);
+        g.seg = seg, g.seg_k = 1, g.M = a.N, g.n_cols = g.N = a.K, g.K = (int)a.M;
+        g.d_expert = (int64_t)a.N * a.K;
+        g.fmt = a.type == kTypeBf16, g.out = a.dw, g.type = g.out_type = a.type, g.vec = a.K % 8 == 0;
+        const Epi ep = epilogue_of(g);
+        split_out(g, f.dw.splits, (int)((a.M + kBk - 1) / kBk), a.K, ws + f.planes);
+        if (a.E == 0)
+            g.seg_k = 0; // one segment: k ends with the rows, where the copies read zeros
+        g.nt = (a.K + f.dw.bn - 1) / f.dw.bn;
+        g.mt = (a.N + kTileM - 1) / kTileM;
+        if ((rc = run_gemm<true, true>(g, f.dw.bn, oa, ob, (int64_t)g.mt * g.nt * (a.E ? a.E : g.splits), s)))
+            return rc;
+        if (g.splits > 1)
+            return launch_reduce(reinterpret_cast<float *>(ws + f.planes), g.splits, a.N, ep, s);
     }
     return MOE_MX_OK;
+}
+
+int linear_status(cudaStream_t s)
+{
+    cudaError_t ce = cudaStreamSynchronize(s);
+    if (ce != cudaSuccess)
+        return cuda_fail(ce, "cudaStreamSynchronize");
+    uint32_t word = 0;
+    if ((ce = cudaMemcpyFromSymbol(&word, g_linear_err, sizeof(word))) != cudaSuccess)
+        return cuda_fail(ce, "cudaMemcpyFromSymbol(error word)");
+    if (word == 0)
+        return MOE_MX_OK;
+    const uint32_t zero = 0;
+    cudaMemcpyToSymbol(g_linear_err, &zero, sizeof(zero));
+    return fail(MOE_MX_ERR_TIMEOUT, "a device-side wait gave up (error word 0x%x)", word);
 }
 
 } // namespace moe_mx

@@ -61,5 +61,7 @@ int64_t linear_backward_workspace(int E, int64_t M, int N, int K, int act, int t
 // MOE_MX_OK or a negative status (text recorded).
 int launch_linear(const LinearArgs &a, cudaStream_t s);
 int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s);
+// Synchronises s; MOE_MX_ERR_TIMEOUT if a wait of the current device's products gave up.
+int linear_status(cudaStream_t s);
 
 } // namespace moe_mx

@@ -79,6 +79,7 @@ SIGNATURES = {
     "moe_mx_linear_workspace": (_I64, [_I, _I64] + [_I] * 5),
     "moe_mx_linear_backward": (_I, [_P] * 6 + [_I, _I64] + [_I] * 5 + [_P, _P, _P, _P, _I64, _P]),
     "moe_mx_linear_backward_workspace": (_I64, [_I, _I64] + [_I] * 5),
+    "moe_mx_linear_status": (_I, [_I, _P]),
 }
 STAGES = ("route", "gather", "fc1", "fc2", "combine")
 
@@ -303,6 +304,11 @@ def moe_mx_linear_backward(dout, x, w, preact, counts, pad_offsets, num_experts:
     _check(load_library().moe_mx_linear_backward(
         _ptr(dout), _ptr(x), _ptr(w), _ptr(preact), _ptr(counts), _ptr(pad_offsets), num_experts, rows, N, K, dtype,
         activation, dout_dtype, _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def moe_mx_linear_status(device: int, stream=None) -> int:
+    """Returns the status code (does not raise on MOE_MX_ERR_TIMEOUT)."""
+    return load_library().moe_mx_linear_status(device, _stream(stream))
 
 
 # ------------------------------------------------------------------ convenience wrappers

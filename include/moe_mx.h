@@ -588,6 +588,13 @@ MOE_MX_API int moe_mx_linear_backward(const void *dout, const void *x, const voi
 MOE_MX_API int64_t moe_mx_linear_backward_workspace(int num_experts, int64_t rows, int N, int K, int dtype,
                                                     int activation, int dout_dtype);
 
+/*
+ * Synchronise `stream` and read the error word of `device`'s linear products: MOE_MX_OK,
+ * MOE_MX_ERR_TIMEOUT if a bounded wait in one of them gave up since the last call (its results are then
+ * incomplete; the word is cleared), or MOE_MX_ERR_CUDA.  Synchronous.  Errors: INVALID_ARG, CUDA.
+ */
+MOE_MX_API int moe_mx_linear_status(int device, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

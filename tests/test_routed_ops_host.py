@@ -75,6 +75,12 @@ def test_workspace_covers_the_largest_calls(lib):
         assert lib.moe_mx_linear_backward_workspace(E, rows, N, K, 0, 1, 0) >= 2 * rows * N
 
 
+def test_workspace_of_no_rows_is_no_error(lib):
+    for E in (0, 4):
+        assert lib.moe_mx_linear_workspace(E, 0, 32, 64, 0, 0, 0) >= 0
+        assert lib.moe_mx_linear_backward_workspace(E, 0, 32, 64, 0, 0, 0) >= 0
+
+
 def _cpu_routing(T=4, k=2, E=4):
     i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
     return ops.Routing(i(T, k), torch.ones(T, k), i(E), i(E + 1), i(T * k), ops.max_grouped_rows(T * k, E))
