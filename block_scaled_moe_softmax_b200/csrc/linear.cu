@@ -381,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int b_row = g.gated ? (int)rank * g.n_cols + t.n0 : t.n0 + (int)rank * (BN / 2);
             for (int kb = 0; kb < t.nkb; ++kb, ++it) {
                 const int s = it % S;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(empty(s), ((it / S) & 1) ^ 1, &g_linear_err, kWaitNs))) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty(s), ((it / S) & 1) ^ 1, &g_linear_err, kWaitNs))) {
                     ok = false;
                     break;
                 }
@@ -395,7 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         bar = map_rank(tail(s), rank);
                         mbar_arrive_expect_tx(tail(s), C::kStage);
                     } else {
-                        mbar_arrive_expect_tx_cluster(bar, C::kStage);
+                        mbar_arrive_expect_tx_relaxed(bar, C::kStage);
                     }
                     const uint32_t sa = base + s * C::kStage, sb = sa + C::kABytes;
                     if (kAMn) {
@@ -420,11 +420,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (it > (uint32_t)j) {
                 const uint32_t last = it - 1 - j;
                 if (rank == 0)
-                    mbar_wait_cluster(full(last % S), (last / S) & 1, nullptr, kDrainNs);
-                mbar_wait_cluster(empty(last % S), (last / S) & 1, nullptr, kDrainNs);
+                    mbar_wait_bounded(full(last % S), (last / S) & 1, nullptr, kDrainNs);
+                mbar_wait_bounded(empty(last % S), (last / S) & 1, nullptr, kDrainNs);
             }
     } else if (warp == 1 && rank == 1) {
-        mbar_wait_cluster(mma_done, 0, nullptr, kDrainNs); // the leader's last commit
+        mbar_wait_bounded(mma_done, 0, nullptr, kDrainNs); // the leader's last commit
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         const uint32_t idesc = idesc_f16(g.fmt, kAMn, kBMn, kTileM, BN);
@@ -434,16 +434,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (t.nkb == 0)
                 continue;
             const int buf = n & 1;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(acc_empty(buf), ((n >> 1) & 1) ^ 1, &g_linear_err, kWaitNs)))
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(acc_empty(buf), ((n >> 1) & 1) ^ 1, &g_linear_err, kWaitNs)))
                 break;
             ++n;
             tc_fence_after();
             for (int kb = 0; kb < t.nkb; ++kb, ++it) {
                 const int s = it % S;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(full(s), (it / S) & 1, &g_linear_err, kWaitNs))) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(full(s), (it / S) & 1, &g_linear_err, kWaitNs))) {
                     ok = false;
                     break;
                 }
+                if (kAMn && t.rem && kb == t.nkb - 1)
+                    fence_acq_cluster(); // the other CTA's tail warp wrote its half by plain stores
                 tc_fence_after();
                 if (elect_lane()) {
                     const uint32_t sa = base + s * C::kStage, sb = sa + C::kABytes;
@@ -465,7 +467,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (elect_lane())
             umma_commit_pair(mma_done);
         __syncwarp();
-        mbar_wait_cluster(mma_done, 0, nullptr, kDrainNs);
+        mbar_wait_bounded(mma_done, 0, nullptr, kDrainNs);
     } else if (warp == 2) {
         // ------------------------------------------------------------ cut k blocks
         if (kAMn && kBMn && g.seg.E) {
@@ -476,7 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!t.rem)
                     continue;
                 const int s = (it - 1) % S;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(tail(s), (ph >> s) & 1, &g_linear_err, kWaitNs))) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(tail(s), (ph >> s) & 1, &g_linear_err, kWaitNs))) {
                     ok = false;
                     break;
                 }
@@ -529,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = pair; get_tile<BN>(g, prefix, i, t); i += pairs) {
             const int buf = n & 1;
             if (t.nkb > 0) {
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(acc_full(buf), (n >> 1) & 1, &g_linear_err, kWaitNs)))
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(acc_full(buf), (n >> 1) & 1, &g_linear_err, kWaitNs)))
                     break;
                 ++n;
                 tc_fence_after();
@@ -560,7 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_cluster(map_rank(acc_empty(buf), 0));
+                    mbar_arrive_relaxed(map_rank(acc_empty(buf), 0)); // TMEM reads are done (wait::ld)
             }
         }
     }

@@ -41,45 +41,25 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes)
+// Arrivals that order none of the thread's memory accesses: for barriers that guard asynchronous copies
+// (whose bytes the barrier counts itself) or TMEM.  A release at cluster scope waits for the thread's
+// earlier copies to land: measured, it held the copies to one k block (about 1500 cycles) at a time.
+__device__ __forceinline__ void mbar_arrive_expect_tx_relaxed(uint32_t bar, uint32_t bytes)
 {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
 
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar)
 {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// mbar_wait_bounded with cluster scope (see ptx.cuh).
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint32_t *err, uint64_t timeout_ns)
+// Orders what another CTA of the cluster released by an arrival that this thread has seen before this
+// thread's later operations.
+__device__ __forceinline__ void fence_acq_cluster()
 {
-    if (mbar_try_wait_cluster(bar, parity))
-        return true;
-    const long long t0 = clock64();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait_cluster(bar, parity))
-            return true;
-        if ((it & 255) == 0) {
-            const unsigned long long dt = (unsigned long long)(clock64() - t0);
-            if (dt > 100000ull && err != nullptr && *(volatile uint32_t *)err != 0)
-                return false;
-            if (dt > timeout_ns) {
-                if (err != nullptr)
-                    atomicOr(err, kErrTimeout);
-                return false;
-            }
-        }
-    }
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 
 // TMA loads into this CTA's shared memory whose bytes are counted on `bar`, a barrier of either CTA
