@@ -18,7 +18,8 @@ namespace moe_mx {
 namespace {
 
 // ---------------------------------------------------------------- activations
-__device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + __expf(-v)); }
+// 1 / (1 + e^-v) to a few ulp (0 once e^-v overflows)
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
 // gelu in its tanh form: 0.5 z (1 + tanh u) = z sigmoid(2u), u = sqrt(2/pi) (z + 0.044715 z^3)
 constexpr float kGelu2A = 1.5957691216057308f; // 2 sqrt(2/pi)
@@ -188,48 +189,6 @@ template <int BN> __device__ __forceinline__ bool get_tile(const Gemm &g, const 
     return true;
 }
 
-// Eight neighbouring values of one row of D: bias, preact, activation, residual, store.
-__device__ __forceinline__ void load8(const void *p, int type, size_t o, float (&f)[8])
-{
-    if (type == kTypeF32) {
-        Raw<float, 8> r;
-        r.load(static_cast<const float *>(p) + o);
-        r.get(f);
-    } else if (type == kTypeF16) {
-        Raw<__half, 8> r;
-        r.load(static_cast<const __half *>(p) + o);
-        r.get(f);
-    } else {
-        Raw<__nv_bfloat16, 8> r;
-        r.load(static_cast<const __nv_bfloat16 *>(p) + o);
-        r.get(f);
-    }
-}
-__device__ __forceinline__ void store8(void *p, int type, size_t o, const float (&f)[8])
-{
-    if (type == kTypeF32)
-        Raw<float, 8>::put(static_cast<float *>(p) + o, f);
-    else if (type == kTypeF16)
-        Raw<__half, 8>::put(static_cast<__half *>(p) + o, f);
-    else
-        Raw<__nv_bfloat16, 8>::put(static_cast<__nv_bfloat16 *>(p) + o, f);
-}
-__device__ __forceinline__ float load1(const void *p, int type, size_t o)
-{
-    return type == kTypeF32   ? static_cast<const float *>(p)[o]
-           : type == kTypeF16 ? __half2float(static_cast<const __half *>(p)[o])
-                              : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[o]);
-}
-__device__ __forceinline__ void store1(void *p, int type, size_t o, float v)
-{
-    if (type == kTypeF32)
-        static_cast<float *>(p)[o] = v;
-    else if (type == kTypeF16)
-        static_cast<__half *>(p)[o] = __float2half_rn(v);
-    else
-        static_cast<__nv_bfloat16 *>(p)[o] = __float2bfloat16_rn(v);
-}
-
 // What the epilogue of a product needs (shared by the kernels).
 struct Epi {
     const float *bias;    // of this expert, or nullptr
@@ -238,70 +197,168 @@ struct Epi {
     int act, N, n_cols, type, out_type, vec;
 };
 
-// z (and up for swiglu): 8 columns of row m from column n.
-__device__ __forceinline__ void finish8(const Epi &g, int64_t m, int n, float (&z)[8], float (&up)[8],
-                                        const float (&bz)[8], const float (&bu)[8], size_t d_off)
-{
-    const bool gated = g.act == kActSwiglu;
-    if (g.bias) {
+// R rows of 8 columns from column n: offsets of the first in out (and residual) and in preact, elements
+// from one to the next, and which are stored (bit j).
+struct Rows {
+    size_t o, po;
+    int so, spo, n;
+    uint32_t ok;
+    __device__ __forceinline__ bool has(int j) const { return (ok >> j) & 1u; }
+    __device__ __forceinline__ size_t at(int j) const { return o + (size_t)j * so; }
+};
+
+// Residual values of R rows x 8 columns, loaded ahead of their use (aligned rows only).
+template <int R> struct Ahead {
+    uint4 a[R], b[R];
+    __device__ __forceinline__ void load(const Epi &g, const Rows &w)
+    {
+        if (!g.residual || !g.vec)
+            return;
+        if (g.out_type == kTypeF32) {
+            const float *p = static_cast<const float *>(g.residual);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            z[i] += bz[i];
-            if (gated)
-                up[i] += bu[i];
+            for (int j = 0; j < R; ++j)
+                if (w.has(j)) {
+                    a[j] = reinterpret_cast<const uint4 *>(p + w.at(j))[0];
+                    b[j] = reinterpret_cast<const uint4 *>(p + w.at(j))[1];
+                }
+        } else {
+            const uint16_t *p = static_cast<const uint16_t *>(g.residual);
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+                if (w.has(j))
+                    a[j] = *reinterpret_cast<const uint4 *>(p + w.at(j));
         }
     }
-    const size_t o = d_off + (size_t)m * g.n_cols + n, po = (size_t)m * g.N + n;
+};
+
+template <typename T, int R>
+__device__ __forceinline__ void add_rows(const Epi &g, const Ahead<R> &ahead, const Rows &w, float (&v)[R][8])
+{
     if (g.vec) {
-        if (g.preact) {
-            store8(g.preact, g.type, po, z);
-            if (gated)
-                store8(g.preact, g.type, po + g.n_cols, up);
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            Raw<T, 8> r;
+            float f[8];
+            if constexpr (sizeof(T) == 4) {
+                r.a = *reinterpret_cast<const float4 *>(&ahead.a[j]);
+                r.b = *reinterpret_cast<const float4 *>(&ahead.b[j]);
+            } else {
+                r.v = ahead.a[j];
+            }
+            r.get(f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) // rows not stored hold what they hold
+                v[j][i] += f[i];
         }
+        return;
+    }
+    const T *p = static_cast<const T *>(g.residual);
+#pragma unroll
+    for (int j = 0; j < R; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            z[i] = gated ? z[i] * sigmoid(z[i]) * up[i] : act_fwd(z[i], g.act);
-        if (g.residual) {
-            float r[8];
-            load8(g.residual, g.out_type, o, r);
+            if (w.has(j) && w.n + i < g.n_cols)
+                v[j][i] += to_f32<T>(p[w.at(j) + i]);
+}
+
+template <typename T, int R>
+__device__ __forceinline__ void put_rows(T *p, int step, const Epi &g, const Rows &w, const float (&v)[R][8])
+{
+    if (g.vec) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                z[i] += r[i];
-        }
-        store8(g.out, g.out_type, o, z);
+        for (int j = 0; j < R; ++j)
+            if (w.has(j))
+                Raw<T, 8>::put(p + (size_t)j * step, v[j]);
         return;
     }
 #pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (w.has(j) && w.n + i < g.n_cols)
+                p[(size_t)j * step + i] = from_f32<T>(v[j][i]);
+}
+
+template <int R>
+__device__ __forceinline__ void put_preact(size_t off, const Epi &g, const Rows &w, const float (&v)[R][8])
+{
+    if (g.type == kTypeF16)
+        put_rows<__half, R>(static_cast<__half *>(g.preact) + off, w.spo, g, w, v);
+    else
+        put_rows<__nv_bfloat16, R>(static_cast<__nv_bfloat16 *>(g.preact) + off, w.spo, g, w, v);
+}
+
+template <int R> __device__ __forceinline__ void add_bias(const float *b, const Epi &g, const Rows &w, float (&v)[R][8])
+{
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (n + i >= g.n_cols)
-            break;
-        if (g.preact) {
-            store1(g.preact, g.type, po + i, z[i]);
-            if (gated)
-                store1(g.preact, g.type, po + g.n_cols + i, up[i]);
-        }
-        float v = gated ? z[i] * sigmoid(z[i]) * up[i] : act_fwd(z[i], g.act);
-        if (g.residual)
-            v += load1(g.residual, g.out_type, o + i);
-        store1(g.out, g.out_type, o + i, v);
+        const float f = w.n + i < g.n_cols ? __ldg(b + w.n + i) : 0.f;
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+            v[j][i] += f;
     }
 }
 
-__device__ __forceinline__ void load_bias8(const Epi &g, int n, float (&bz)[8], float (&bu)[8])
+// Bias, preact, activation, residual and store of z (kGated: swiglu, with up).  Every choice is made
+// once for all rows: choosing per value cost 3000 cycles per 32 x 32 block in branches alone.
+template <int R, bool kGated>
+__device__ __forceinline__ void finish(const Epi &g, const Rows &w, float (&z)[R][8], float (&up)[R][8],
+                                       const Ahead<R> &ahead)
 {
-    if (!g.bias)
-        return;
+    if (g.bias) {
+        add_bias<R>(g.bias, g, w, z);
+        if (kGated)
+            add_bias<R>(g.bias + g.n_cols, g, w, up);
+    }
+    if (g.preact) {
+        put_preact<R>(w.po, g, w, z);
+        if (kGated)
+            put_preact<R>(w.po + g.n_cols, g, w, up);
+    }
+    if (kGated) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const bool in = n + i < g.n_cols;
-        bz[i] = in ? __ldg(g.bias + n + i) : 0.f;
-        bu[i] = in && g.act == kActSwiglu ? __ldg(g.bias + n + i + g.n_cols) : 0.f;
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                z[j][i] *= sigmoid(z[j][i]) * up[j][i];
+    } else if (g.act == kActSilu) {
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                z[j][i] = act_fwd(z[j][i], kActSilu);
+    } else if (g.act == kActGelu) {
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                z[j][i] = act_fwd(z[j][i], kActGelu);
+    }
+    if (g.out_type == kTypeF32) {
+        if (g.residual)
+            add_rows<float, R>(g, ahead, w, z);
+        put_rows<float, R>(static_cast<float *>(g.out) + w.o, w.so, g, w, z);
+    } else if (g.out_type == kTypeF16) {
+        if (g.residual)
+            add_rows<__half, R>(g, ahead, w, z);
+        put_rows<__half, R>(static_cast<__half *>(g.out) + w.o, w.so, g, w, z);
+    } else {
+        if (g.residual)
+            add_rows<__nv_bfloat16, R>(g, ahead, w, z);
+        put_rows<__nv_bfloat16, R>(static_cast<__nv_bfloat16 *>(g.out) + w.o, w.so, g, w, z);
     }
 }
+
+// The tensor core adds into its float32 accumulator by truncation: a chain over K = 7168 is off by
+// 8e-6 in relative norm (measured), where a rounding sum is by 9e-7.  Products with float32 outputs
+// therefore hand the accumulator over every kChain k blocks (kSum) and the epilogue's warps keep
+// the sum in registers; a 2-byte output's own rounding is far larger.
+constexpr int kChain = 8;
 
 __device__ uint32_t g_linear_err; // set by a wait that gave up
 
-template <int BN, bool kAMn, bool kBMn>
+template <int BN, bool kAMn, bool kBMn, bool kSum>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_kernel(const Gemm g, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b)
 {
@@ -431,36 +488,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t it = 0, n = 0;
         bool ok = true;
         for (int i = pair; ok && get_tile<BN>(g, prefix, i, t); i += pairs) {
-            if (t.nkb == 0)
-                continue;
-            const int buf = n & 1;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(acc_empty(buf), ((n >> 1) & 1) ^ 1, &g_linear_err, kWaitNs)))
-                break;
-            ++n;
-            tc_fence_after();
-            for (int kb = 0; kb < t.nkb; ++kb, ++it) {
-                const int s = it % S;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(full(s), (it / S) & 1, &g_linear_err, kWaitNs))) {
+            for (int kb = 0; ok && kb < t.nkb;) {
+                const int buf = n & 1;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(acc_empty(buf), ((n >> 1) & 1) ^ 1, &g_linear_err, kWaitNs))) {
                     ok = false;
                     break;
                 }
-                if (kAMn && t.rem && kb == t.nkb - 1)
-                    fence_acq_cluster(); // the other CTA's tail warp wrote its half by plain stores
+                ++n;
                 tc_fence_after();
-                if (elect_lane()) {
-                    const uint32_t sa = base + s * C::kStage, sb = sa + C::kABytes;
-                    const uint64_t da = kAMn ? smem_desc_mn_sw128(sa, 8192) : smem_desc_sw128(sa);
-                    const uint64_t db = kBMn ? smem_desc_mn_sw128(sb, 8192) : smem_desc_sw128(sb);
-                    // 16 of k: 32 bytes of a K-major row, or two 1024-byte groups of 8 k
+                const int first = kb, end = kSum ? min(t.nkb, kb + kChain) : t.nkb;
+                for (; kb < end; ++kb, ++it) {
+                    const int s = it % S;
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(full(s), (it / S) & 1, &g_linear_err, kWaitNs))) {
+                        ok = false;
+                        break;
+                    }
+                    if (kAMn && t.rem && kb == t.nkb - 1)
+                        fence_acq_cluster(); // the other CTA's tail warp wrote its half by plain stores
+                    tc_fence_after();
+                    if (elect_lane()) {
+                        const uint32_t sa = base + s * C::kStage, sb = sa + C::kABytes;
+                        const uint64_t da = kAMn ? smem_desc_mn_sw128(sa, 8192) : smem_desc_sw128(sa);
+                        const uint64_t db = kBMn ? smem_desc_mn_sw128(sb, 8192) : smem_desc_sw128(sb);
+                        // 16 of k: 32 bytes of a K-major row, or two 1024-byte groups of 8 k
 #pragma unroll
-                    for (int q = 0; q < kBk / 16; ++q)
-                        umma_f16_pair(tmem + 256u * buf, da + q * (kAMn ? 128 : 2), db + q * (kBMn ? 128 : 2), idesc,
-                                      kb > 0 || q > 0);
-                    umma_commit_pair(empty(s));
-                    if (kb == t.nkb - 1)
-                        umma_commit_pair(acc_full(buf));
+                        for (int q = 0; q < kBk / 16; ++q)
+                            umma_f16_pair(tmem + 256u * buf, da + q * (kAMn ? 128 : 2), db + q * (kBMn ? 128 : 2),
+                                          idesc, kb > first || q > 0);
+                        umma_commit_pair(empty(s));
+                        if (kb == end - 1)
+                            umma_commit_pair(acc_full(buf));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
         }
         // every MMA has completed before TMEM is released
@@ -502,67 +562,144 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int cols = g.gated ? BN / 4 : BN / 2; // columns of D this warp takes
         const int rl = lane >> 2, c8 = (lane & 3) * 8;
         uint32_t n = 0;
-        // accumulator columns [c, c + 32) of this warp's 32 rows, through shared memory: lane l then
-        // holds row 8 it + l / 4, columns 8 (l % 4) .. + 7
-        auto chunk = [&](uint32_t c, float (&v)[4][8]) {
-            uint32_t r0[16], r1[16];
-            tmem_ld16(c, r0);
-            tmem_ld16(c + 16, r1);
-            tmem_wait_ld();
+        bool ok = true;
+        // 32 columns of this warp's 32 rows (lane: row) through shared memory: lane l then holds row
+        // 8 j + l / 4, columns 8 (l % 4) .. + 7
+        auto turn = [&](const uint32_t (&r)[32], float (&v)[4][8]) {
+            float4 *own = reinterpret_cast<float4 *>(stg + lane * 32);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float4 *row = reinterpret_cast<float4 *>(stg + lane * 32);
-                row[j ^ (lane & 7)] = make_float4(__uint_as_float(r0[4 * j]), __uint_as_float(r0[4 * j + 1]),
-                                                  __uint_as_float(r0[4 * j + 2]), __uint_as_float(r0[4 * j + 3]));
-                row[(j + 4) ^ (lane & 7)] = make_float4(__uint_as_float(r1[4 * j]), __uint_as_float(r1[4 * j + 1]),
-                                                        __uint_as_float(r1[4 * j + 2]), __uint_as_float(r1[4 * j + 3]));
-            }
+            for (int j = 0; j < 8; ++j)
+                own[j ^ (lane & 7)] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                                  __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = i * 8 + rl;
-                const float4 *row = reinterpret_cast<const float4 *>(stg + r * 32);
-                const float4 a = row[(c8 / 4) ^ (r & 7)], b = row[(c8 / 4 + 1) ^ (r & 7)];
+                const int row = i * 8 + rl;
+                const float4 *src = reinterpret_cast<const float4 *>(stg + row * 32);
+                const float4 a = src[(c8 / 4) ^ (row & 7)], b = src[(c8 / 4 + 1) ^ (row & 7)];
                 v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
                 v[i][4] = b.x, v[i][5] = b.y, v[i][6] = b.z, v[i][7] = b.w;
             }
             __syncwarp();
         };
-        for (int i = pair; get_tile<BN>(g, prefix, i, t); i += pairs) {
-            const int buf = n & 1;
-            if (t.nkb > 0) {
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(acc_full(buf), (n >> 1) & 1, &g_linear_err, kWaitNs)))
-                    break;
-                ++n;
-                tc_fence_after();
-            }
-            Epi ep{g.bias ? g.bias + (size_t)t.e * g.N : nullptr, g.residual, g.out, g.preact, g.act, g.N, g.n_cols,
-                   g.type, g.out_type, g.vec};
+        // Accumulator n of this pair is complete; `free_acc` gives its TMEM back to the MMAs.
+        auto wait_acc = [&]() {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(acc_full(n & 1), (n >> 1) & 1, &g_linear_err, kWaitNs));
+            tc_fence_after();
+            return ok;
+        };
+        auto free_acc = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_relaxed(map_rank(acc_empty(n & 1), 0)); // its TMEM reads are done (wait::ld)
+            ++n;
+        };
+        for (int i = pair; ok && get_tile<BN>(g, prefix, i, t); i += pairs) {
+            // gradients have no bias, preact, activation or residual
+            const Epi ep = kBMn ? Epi{nullptr, nullptr, g.out, nullptr, kActNone, g.N, g.n_cols, g.type, g.out_type, g.vec}
+                                : Epi{g.bias ? g.bias + (size_t)t.e * g.N : nullptr, g.residual, g.out, g.preact, g.act,
+                                      g.N, g.n_cols, g.type, g.out_type, g.vec};
             const size_t d_off = g.seg_k ? (size_t)t.e * g.d_expert : (size_t)t.split * g.M * g.n_cols;
-            const uint32_t acc = tmem + 256u * buf + ((uint32_t)(q * 32) << 16);
-            for (int c = 0; c < cols; c += 32) {
-                const int lc = half * cols + c; // column within the tile
-                float v[4][8] = {}, up[4][8] = {}, bz[8], bu[8];
-                const int nn = t.n0 + lc + c8;
-                load_bias8(ep, nn, bz, bu);
-                if (t.nkb > 0) {
-                    chunk(acc + lc, v);
-                    if (g.gated)
-                        chunk(acc + BN / 2 + lc, up);
-                }
-                if (nn < g.n_cols)
+            const int row0 = t.row + (int)rank * 128 + q * 32 + rl;
+            Ahead<4> ahead;
+            Rows w;
+            w.so = 8 * g.n_cols, w.spo = 8 * g.N;
+            auto place = [&](int c) { // this lane's four rows at column c of the tile
+                w.n = t.n0 + c + c8;
+                w.ok = 0;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int64_t m = (int64_t)t.row + (int)rank * 128 + q * 32 + j * 8 + rl;
-                        if (m < t.row_end)
-                            finish8(ep, m, nn, v[j], up[j], bz, bu, d_off);
+                for (int j = 0; j < 4; ++j)
+                    w.ok |= row0 + j * 8 < t.row_end && w.n < g.n_cols ? 1u << j : 0u;
+                w.o = d_off + (size_t)row0 * g.n_cols + w.n;
+                w.po = (size_t)row0 * g.N + w.n;
+                ahead.load(ep, w);
+            };
+            const uint32_t lanes = (uint32_t)(q * 32) << 16;
+            if constexpr (kSum) {
+                // columns lc .. of D (gated: and the same of the up half) summed over the chains
+                constexpr int kChunks = BN / 64;
+                uint32_t sum[kChunks][32];
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        sum[c][x] = 0u;
+                // chunk c's first accumulator column: this warp's half, or its gate and up columns
+                auto acc_col = [&](int c) {
+                    return g.gated ? (c % (kChunks / 2)) * 32 + half * (BN / 4) + (c >= kChunks / 2 ? BN / 2 : 0)
+                                   : half * (BN / 2) + c * 32;
+                };
+                for (int kb = 0; ok && kb < t.nkb; kb += kChain) {
+                    if (!wait_acc())
+                        break;
+                    const uint32_t acc = tmem + 256u * (n & 1) + lanes;
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        uint32_t r0[16], r1[16];
+                        tmem_ld16(acc + acc_col(c), r0);
+                        tmem_ld16(acc + acc_col(c) + 16, r1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            sum[c][x] = __float_as_uint(__uint_as_float(sum[c][x]) + __uint_as_float(r0[x]));
+                            sum[c][x + 16] = __float_as_uint(__uint_as_float(sum[c][x + 16]) + __uint_as_float(r1[x]));
+                        }
                     }
-            }
-            if (t.nkb > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_relaxed(map_rank(acc_empty(buf), 0)); // TMEM reads are done (wait::ld)
+                    free_acc();
+                }
+                if (!ok)
+                    break;
+                if (g.gated) {
+                    if constexpr (kChunks % 2 == 0) {
+#pragma unroll
+                        for (int c = 0; c < kChunks / 2; ++c) {
+                            float v[4][8], up[4][8];
+                            const int lc = half * cols + c * 32;
+                            place(lc);
+                            turn(sum[c], v);
+                            turn(sum[c + kChunks / 2], up);
+                            finish<4, true>(ep, w, v, up, ahead);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        float v[4][8], up[4][8];
+                        const int lc = half * cols + c * 32;
+                        place(lc);
+                        turn(sum[c], v);
+                        finish<4, false>(ep, w, v, up, ahead);
+                    }
+                }
+            } else {
+                auto take = [&](uint32_t col, float (&f)[4][8]) {
+                    uint32_t r[32];
+                    tmem_ld32(tmem + 256u * (n & 1) + lanes + col, r);
+                    tmem_wait_ld();
+                    turn(r, f);
+                };
+                for (int c = 0; c < cols; c += 32) {
+                    const int lc = half * cols + c; // column within the tile
+                    place(lc);
+                    if (c == 0 && t.nkb > 0 && !wait_acc())
+                        break;
+                    float v[4][8] = {}, up[4][8] = {};
+                    if (t.nkb > 0)
+                        take(lc, v);
+                    if (!kBMn && g.gated) {
+                        if (t.nkb > 0) {
+                            take(BN / 2 + lc, up);
+                            if (c + 32 >= cols)
+                                free_acc();
+                        }
+                        finish<4, true>(ep, w, v, up, ahead);
+                    } else {
+                        if (t.nkb > 0 && c + 32 >= cols)
+                            free_acc();
+                        finish<4, false>(ep, w, v, up, ahead);
+                    }
+                }
             }
         }
     }
@@ -578,6 +715,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- split products
+__device__ __forceinline__ void load_f32x8(const float *p, float (&f)[8])
+{
+    Raw<float, 8> r;
+    r.load(p);
+    r.get(f);
+}
+
 // out = epilogue(sum over the splits' float32 planes, in order); one thread per 8 columns of a row.
 __global__ void __launch_bounds__(256) reduce_kernel(const float *__restrict__ planes, int splits, int M, Epi g)
 {
@@ -591,33 +735,38 @@ __global__ void __launch_bounds__(256) reduce_kernel(const float *__restrict__ p
     const int n = (int)(i % per_row) * 8;
     const bool gated = g.act == kActSwiglu;
     const size_t plane = (size_t)M * g.N;
-    float z[8] = {}, up[8] = {}, bz[8], bu[8];
-    load_bias8(g, n, bz, bu);
+    float z[1][8] = {}, up[1][8] = {};
+    const Rows w{(size_t)m * g.n_cols + n, (size_t)m * g.N + n, 0, 0, n, 1u};
+    Ahead<1> ahead;
+    ahead.load(g, w);
     for (int s = 0; s < splits; ++s) {
         const float *p = planes + s * plane + m * g.N + n;
         if (g.vec) {
             float f[8];
-            load8(p, kTypeF32, 0, f);
+            load_f32x8(p, f);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                z[j] += f[j];
+                z[0][j] += f[j];
             if (gated) {
-                load8(p, kTypeF32, g.n_cols, f);
+                load_f32x8(p + g.n_cols, f);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    up[j] += f[j];
+                    up[0][j] += f[j];
             }
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (n + j < g.n_cols) {
-                    z[j] += p[j];
+                    z[0][j] += p[j];
                     if (gated)
-                        up[j] += p[j + g.n_cols];
+                        up[0][j] += p[j + g.n_cols];
                 }
         }
     }
-    finish8(g, m, n, z, up, bz, bu, 0);
+    if (gated)
+        finish<1, true>(g, w, z, up, ahead);
+    else
+        finish<1, false>(g, w, z, up, ahead);
 }
 
 // ---------------------------------------------------------------- unaligned rows
@@ -648,10 +797,11 @@ constexpr int kPairs = 74; // SM pairs of the 148-SM part the plans are made for
 // writes and reads its float32 planes and launches a second kernel.
 struct Plan {
     int bn, splits;
+    bool sum; // the sum over chains of kChain k blocks kept in registers (at most 192 columns wide)
 };
-Plan plan_dense(int64_t M, int cols, int kb, bool gated, bool mn)
+Plan plan_dense(int64_t M, int cols, int kb, bool gated, bool mn, bool f32)
 {
-    Plan best{256, 1};
+    Plan best{256, 1, false};
     if (kb == 0)
         return best;
     double best_t = 1e30;
@@ -663,21 +813,24 @@ Plan plan_dense(int64_t M, int cols, int kb, bool gated, bool mn)
             if (s > 1 && kb / s < 4)
                 break;
             const int64_t kbs = (kb + s - 1) / s;
+            const bool sum = f32 && kbs > kChain;
+            if (sum && bn == 256)
+                continue;
             const int64_t tiles = mt * ((cols + bn - 1) / bn) * ((kb + kbs - 1) / kbs);
             double t = (double)((tiles + kPairs - 1) / kPairs) * ((double)kbs * (256 + bn) + 1500);
             if (s > 1)
                 t += 5000 + (double)s * M * cols * 8 / 4000;
             if (t < best_t)
-                best_t = t, best = Plan{bn, s};
+                best_t = t, best = Plan{bn, s, sum};
         }
     }
     return best;
 }
 
-template <int BN, bool kAMn, bool kBMn>
+template <int BN, bool kAMn, bool kBMn, bool kSum>
 int launch_gemm(const Gemm &g, const CUtensorMap &ma, const CUtensorMap &mb, int tiles, cudaStream_t s)
 {
-    auto kernel = gemm_kernel<BN, kAMn, kBMn>;
+    auto kernel = gemm_kernel<BN, kAMn, kBMn, kSum>;
     // per device and cheap; nothing to remember between calls
     cudaError_t ce = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::kSmem);
     if (ce != cudaSuccess)
@@ -704,7 +857,7 @@ int make_map(CUtensorMap *map, const Operand &o, int box_rows, bool three)
 
 // tiles: an upper bound of the product's tiles (the kernel finds a grouped product's on the device)
 template <bool kAMn, bool kBMn>
-int run_gemm(Gemm &g, int bn, const Operand &a, const Operand &b, int64_t tiles, cudaStream_t s)
+int run_gemm(Gemm &g, int bn, bool sum, const Operand &a, const Operand &b, int64_t tiles, cudaStream_t s)
 {
     if (tiles > INT32_MAX)
         return fail(MOE_MX_ERR_UNSUPPORTED, "the product has %lld tiles", (long long)tiles);
@@ -712,12 +865,16 @@ int run_gemm(Gemm &g, int bn, const Operand &a, const Operand &b, int64_t tiles,
     int rc;
     if ((rc = make_map(&ma, a, kAMn ? 64 : 128, false)) || (rc = make_map(&mb, b, kBMn ? 64 : bn / 2, true)))
         return rc;
+    if constexpr (!kBMn)
+        if (sum)
+            return bn == 192 ? launch_gemm<192, kAMn, kBMn, true>(g, ma, mb, (int)tiles, s)
+                             : launch_gemm<128, kAMn, kBMn, true>(g, ma, mb, (int)tiles, s);
     if (bn == 256)
-        return launch_gemm<256, kAMn, kBMn>(g, ma, mb, (int)tiles, s);
+        return launch_gemm<256, kAMn, kBMn, false>(g, ma, mb, (int)tiles, s);
     if constexpr (!kBMn)
         if (bn == 192)
-            return launch_gemm<192, kAMn, kBMn>(g, ma, mb, (int)tiles, s);
-    return launch_gemm<128, kAMn, kBMn>(g, ma, mb, (int)tiles, s);
+            return launch_gemm<192, kAMn, kBMn, false>(g, ma, mb, (int)tiles, s);
+    return launch_gemm<128, kAMn, kBMn, false>(g, ma, mb, (int)tiles, s);
 }
 
 // ---------------------------------------------------------------- dz and the bias gradient
@@ -841,16 +998,17 @@ struct ForwardPlan {
     Plan p;
     int64_t x, w, planes, bytes;
 };
-ForwardPlan plan_linear(int E, int64_t M, int N, int K, int act)
+ForwardPlan plan_linear(int E, int64_t M, int N, int K, int act, bool f32)
 {
     ForwardPlan f{};
     const bool gated = act == kActSwiglu;
     const int kb = (K + kBk - 1) / kBk;
     if (E == 0) {
         // a gated product is one of N columns in tiles of the gate's and the up's; a split one is plain
-        f.p = plan_dense(M, N, kb, gated, false);
+        f.p = plan_dense(M, N, kb, gated, false, f32);
     } else {
-        f.p = Plan{N > 128 ? 256 : 128, 1};
+        const bool sum = f32 && kb > kChain;
+        f.p = Plan{N <= 128 || (sum && gated) ? 128 : sum ? 192 : 256, 1, sum};
     }
     Parts ws;
     f.x = ws.take(K % 8 ? M * round_up(K, 8) * 2 : 0);
@@ -869,9 +1027,9 @@ BackwardPlan plan_backward(int E, int64_t M, int N, int K, int act, int type, in
 {
     BackwardPlan f{};
     f.direct = dz_is_dout(act, type, dout_type, N);
-    f.dw = Plan{256, 1};
+    f.dw = Plan{256, 1, false};
     if (E == 0)
-        f.dw = plan_dense(N, K, (int)((M + kBk - 1) / kBk), false, true);
+        f.dw = plan_dense(N, K, (int)((M + kBk - 1) / kBk), false, true, false);
     Parts ws;
     f.part = ws.take((M + 127) / 128 * N * 4);
     f.dz = ws.take(f.direct ? 0 : M * ldz_of(N) * 2);
@@ -919,9 +1077,9 @@ void split_out(Gemm &g, int splits, int kb, int N, void *planes)
 
 } // namespace
 
-int64_t linear_workspace(int E, int64_t M, int N, int K, int act, int, int)
+int64_t linear_workspace(int E, int64_t M, int N, int K, int act, int, int out_type)
 {
-    return plan_linear(E, M, N, K, act).bytes;
+    return plan_linear(E, M, N, K, act, out_type == kTypeF32).bytes;
 }
 
 int64_t linear_backward_workspace(int E, int64_t M, int N, int K, int act, int type, int dout_type)
@@ -931,7 +1089,7 @@ int64_t linear_backward_workspace(int E, int64_t M, int N, int K, int act, int t
 
 int launch_linear(const LinearArgs &a, cudaStream_t s)
 {
-    const ForwardPlan f = plan_linear(a.E, a.M, a.N, a.K, a.act);
+    const ForwardPlan f = plan_linear(a.E, a.M, a.N, a.K, a.act, a.out_type == kTypeF32);
     char *ws = static_cast<char *>(a.ws);
     const int ld = (int)round_up(a.K, 8), experts = a.E ? a.E : 1;
     const Operand x{packed(a.x, a.M, a.K, ws, f.x, s), a.K, a.M, ld, 1};
@@ -950,7 +1108,7 @@ int launch_linear(const LinearArgs &a, cudaStream_t s)
     g.mt = (int)((a.M + kTileM - 1) / kTileM);
     // grouped: every expert hit has at most one part-filled row tile
     const int64_t mt = a.E ? a.M / kTileM + a.E : g.mt;
-    const int rc = run_gemm<false, false>(g, f.p.bn, x, w, mt * g.nt * g.splits, s);
+    const int rc = run_gemm<false, false>(g, f.p.bn, f.p.sum, x, w, mt * g.nt * g.splits, s);
     if (rc || g.splits == 1)
         return rc;
     return launch_reduce(reinterpret_cast<float *>(ws + f.planes), g.splits, a.M, ep, s);
@@ -1004,7 +1162,7 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
         g.nt = (a.K + bn - 1) / bn;
         g.mt = (int)((a.M + kTileM - 1) / kTileM);
         const int64_t mt = a.E ? a.M / kTileM + a.E : g.mt;
-        if ((rc = run_gemm<false, true>(g, bn, oa, ob, mt * g.nt, s)))
+        if ((rc = run_gemm<false, true>(g, bn, false, oa, ob, mt * g.nt, s)))
             return rc;
     }
     if (a.dw) {
@@ -1024,7 +1182,7 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
             g.seg_k = 0; // one segment: k ends with the rows, where the copies read zeros
         g.nt = (a.K + f.dw.bn - 1) / f.dw.bn;
         g.mt = (a.N + kTileM - 1) / kTileM;
-        if ((rc = run_gemm<true, true>(g, f.dw.bn, oa, ob, (int64_t)g.mt * g.nt * (a.E ? a.E : g.splits), s)))
+        if ((rc = run_gemm<true, true>(g, f.dw.bn, false, oa, ob, (int64_t)g.mt * g.nt * (a.E ? a.E : g.splits), s)))
             return rc;
         if (g.splits > 1)
             return launch_reduce(reinterpret_cast<float *>(ws + f.planes), g.splits, a.N, ep, s);
