@@ -73,7 +73,7 @@ int encode_nd(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *pt
     EncodeTiledFn enc = get_encode_fn();
     if (!enc)
         return fail(MOE_MX_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    const cuuint32_t estr[3] = {1, 1, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     const CUresult r = enc(map, dt, rank, const_cast<void *>(ptr), dims, strides, box, estr,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

@@ -17,7 +17,7 @@ constexpr int kMaxDim = 1 << 20;      // hidden, N, K
 
 bool type_ok(int t) { return t == MOE_MX_TYPE_BF16 || t == MOE_MX_TYPE_F32 || t == MOE_MX_TYPE_F16; }
 
-// The device of a call: the one that holds its first tensor.
+// The device of a call: the one that holds its first tensor, which is checked like the others.
 int device_of(const void *p, const char *name, int *dev)
 {
     cudaPointerAttributes at;
@@ -26,6 +26,8 @@ int device_of(const void *p, const char *name, int *dev)
         cudaGetLastError();
         return fail(MOE_MX_ERR_INVALID_ARG, "%s must be a device pointer", name);
     }
+    if (reinterpret_cast<uintptr_t>(p) % 16 != 0)
+        return fail(MOE_MX_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
     *dev = at.device;
     return MOE_MX_OK;
 }
@@ -117,7 +119,7 @@ int moe_mx_dispatch(const void *x, int num_tokens, int hidden, int top_k, const 
     if (rc || num_tokens == 0)
         return rc;
     int dev;
-    if ((rc = device_of(x, "x", &dev)) || (rc = check_ptr(x, dev, "x")) ||
+    if ((rc = device_of(x, "x", &dev)) ||
         (rc = check_ptr(pos_of_pair, dev, "pos_of_pair")) || (rc = check_ptr(grouped, dev, "grouped")))
         return rc;
     if (overlap(x, (size_t)num_tokens * hidden * type_bytes(dtype), grouped, (size_t)rows * hidden * type_bytes(dtype)))
@@ -142,7 +144,7 @@ int moe_mx_combine(const void *grouped, int64_t rows, int num_tokens, int hidden
     if (num_tokens == 0)
         return MOE_MX_OK;
     int dev;
-    if ((rc = device_of(out, "out", &dev)) || (rc = check_ptr(out, dev, "out")) ||
+    if ((rc = device_of(out, "out", &dev)) ||
         (rc = check_ptr(grouped, dev, "grouped")) || (rc = check_ptr(pos_of_pair, dev, "pos_of_pair")) ||
         (topk_w && (rc = check_ptr(topk_w, dev, "topk_w"))))
         return rc;
@@ -175,7 +177,7 @@ int moe_mx_combine_backward(const void *dout, const void *grouped, int64_t rows,
     if (num_tokens == 0)
         return MOE_MX_OK;
     int dev;
-    if ((rc = device_of(dout, "dout", &dev)) || (rc = check_ptr(dout, dev, "dout")) ||
+    if ((rc = device_of(dout, "dout", &dev)) ||
         (rc = check_ptr(pos_of_pair, dev, "pos_of_pair")) || (rc = check_ptr(topk_w, dev, "topk_w")) ||
         (dgrouped && (rc = check_ptr(dgrouped, dev, "dgrouped"))) ||
         ((dtopk_w || dlogits) && (rc = check_ptr(grouped, dev, "grouped"))) ||
@@ -224,7 +226,7 @@ int moe_mx_linear(const void *x, const void *w, const float *bias, const void *r
     if (rc || rows == 0)
         return rc;
     int dev;
-    if ((rc = device_of(x, "x", &dev)) || (rc = check_ptr(x, dev, "x")) || (rc = check_ptr(w, dev, "w")) ||
+    if ((rc = device_of(x, "x", &dev)) || (rc = check_ptr(w, dev, "w")) ||
         (rc = check_ptr(out, dev, "out")) || (bias && (rc = check_ptr(bias, dev, "bias"))) ||
         (residual && (rc = check_ptr(residual, dev, "residual"))) ||
         (preact && (rc = check_ptr(preact, dev, "preact"))) ||
@@ -278,7 +280,7 @@ int moe_mx_linear_backward(const void *dout, const void *x, const void *w, const
         return fail(MOE_MX_ERR_INVALID_ARG, "preact must be given for an activation");
     int dev;
     const bool some = rows > 0; // with no rows only the zero gradients dw and dbias are written
-    if (some && ((rc = device_of(dout, "dout", &dev)) || (rc = check_ptr(dout, dev, "dout"))))
+    if (some && ((rc = device_of(dout, "dout", &dev))))
         return rc;
     if (!some) {
         if (!dw && !dbias)

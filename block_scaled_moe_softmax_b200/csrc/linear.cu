@@ -103,13 +103,19 @@ template <typename F> void by_half(int type, F f)
 //
 // Operands with k contiguous (x and w of the forward pass, dz in dx) are K-major tiles; those with
 // k along the rows (w in dx; dz and x in dw) are read as they lie, as M- or N-major tiles.
+//
+// kSwap computes the transpose of a tile: 256 weight rows are the A operand and the tokens the B
+// operand, as many of them (a multiple of 32, up to 256) as the tile has.  A segment of 40 tokens then
+// costs the MMAs of 64 tokens and loads no rows of padding, where a tile of 256 token rows takes all
+// of them: the grouped products and small dense ones run so.
 struct Gemm {
     Segments seg;
     int seg_k;            // the segments run over k (dw) instead of the rows
     int M, n_cols, K;     // rows and columns of D, depth (dense, or of a rows-segmented product)
     int kb_split;         // k blocks of one split (dense only), split s writes plane s of out
     int mt, nt, splits;   // tiles of a dense product, or of one expert's when the segments run over k
-    int gated;            // swiglu: the pair's CTAs take the gate and the up rows of B
+    int tok;              // kSwap, dense: tokens of a tile
+    int gated;            // swiglu: gate and up rows in one tile (of B halves; kSwap: 16 by 16 rows of A)
     int fmt;              // 0: f16, 1: bf16
     // epilogue
     const float *bias;
@@ -139,13 +145,23 @@ struct Tile {
     int n0;              // first column of D
     int k0, nkb, rem;    // first k (element), k blocks, valid rows of the last (0: all)
     int split;
+    int tok;             // kSwap: tokens of the tile, a multiple of 32
 };
 
-// The t-th tile.  Rows-segmented: prefix[e] holds the number of tiles of the experts before e, tiles run
-// over an expert's row tiles first, so that neighbouring pairs read the same rows of B.
-template <int BN> __device__ __forceinline__ bool get_tile(const Gemm &g, const int32_t *prefix, int t, Tile &o)
+// Token tiles of a segment, equally long: at most `most` tokens each, rounded up to 32.
+__device__ __forceinline__ int token_tiles(int rows, int most, int &tok)
 {
-    const int bn = g.gated ? BN / 2 : BN;
+    const int tiles = (rows + most - 1) / most;
+    tok = tiles ? ((rows + tiles - 1) / tiles + 31) / 32 * 32 : 0;
+    return tiles;
+}
+
+// The t-th tile.  Rows-segmented: prefix[e] holds the number of tiles of the experts before e, tiles run
+// over an expert's row tiles first, so that neighbouring pairs read the same weights.
+template <int BN, bool kSwap, int kMostTok>
+__device__ __forceinline__ bool get_tile(const Gemm &g, const int32_t *prefix, int t, Tile &o)
+{
+    const int bn = g.gated ? (kSwap ? 128 : BN / 2) : BN; // columns of D in a tile
     o.rem = 0, o.split = 0;
     if (g.seg.E == 0) {
         const int per = g.mt * g.nt;
@@ -153,12 +169,13 @@ template <int BN> __device__ __forceinline__ bool get_tile(const Gemm &g, const 
         if (o.split >= g.splits)
             return false;
         t -= o.split * per;
-        o.e = 0, o.row = t % g.mt * kTileM, o.row_end = g.M, o.n0 = t / g.mt * bn;
+        o.e = 0, o.row = t % g.mt * (kSwap ? g.tok : kTileM), o.row_end = g.M, o.n0 = t / g.mt * bn;
+        o.tok = min(g.tok, (g.M - o.row + 31) / 32 * 32);
         const int kb = (g.K + kBk - 1) / kBk, lo = o.split * g.kb_split;
         o.k0 = lo * kBk, o.nkb = min(g.kb_split, kb - lo);
         return true;
     }
-    if (g.seg_k) {
+    if (!kSwap && g.seg_k) {
         const int per = g.mt * g.nt;
         o.e = t / per;
         if (o.e >= g.seg.E)
@@ -180,11 +197,12 @@ template <int BN> __device__ __forceinline__ bool get_tile(const Gemm &g, const 
         else
             hi = mid;
     }
-    int first;
+    int first, tok = kTileM;
     const int rows = segment_rows(g.seg, lo, first);
-    const int mt = (rows + kTileM - 1) / kTileM;
+    const int mt = kSwap ? token_tiles(rows, kMostTok, tok) : (rows + kTileM - 1) / kTileM;
     t -= prefix[lo];
-    o.e = lo, o.row = first + t % mt * kTileM, o.row_end = first + rows, o.n0 = t / mt * bn;
+    o.e = lo, o.row = first + t % mt * tok, o.row_end = first + rows, o.n0 = t / mt * bn;
+    o.tok = min(tok, (o.row_end - o.row + 31) / 32 * 32);
     o.k0 = 0, o.nkb = (g.K + kBk - 1) / kBk;
     return true;
 }
@@ -358,11 +376,14 @@ constexpr int kChain = 8;
 
 __device__ uint32_t g_linear_err; // set by a wait that gave up
 
-template <int BN, bool kAMn, bool kBMn, bool kSum>
+template <int BN, bool kAMn, bool kBMn, bool kSum, bool kSwap>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    gemm_kernel(const Gemm g, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b)
+    gemm_kernel(const Gemm g, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                const __grid_constant__ CUtensorMap map_c)
 {
     using C = Cfg<BN>;
+    constexpr bool kPlain = kSwap ? kAMn : kBMn;  // a gradient: no bias, preact, activation or residual
+    constexpr int kMostTok = kSum ? 128 : 256;    // kSwap: tokens of a tile (kSum keeps them in registers)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *const sm = smem_raw + (base - smem_u32(smem_raw));
@@ -392,6 +413,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_mbar_init();
         prefetch_tensormap(&map_a);
         prefetch_tensormap(&map_b);
+        if (kSwap)
+            prefetch_tensormap(&map_c);
     }
     if (warp == 2)
         tmem_alloc_pair(tmem_slot, 512);
@@ -405,7 +428,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (e < g.seg.E) {
                 int first;
                 const int rows = segment_rows(g.seg, e, first);
-                n = (rows + kTileM - 1) / kTileM * g.nt;
+                int tok;
+                n = (kSwap ? token_tiles(rows, kMostTok, tok) : (rows + kTileM - 1) / kTileM) * g.nt;
             }
             int incl = n;
 #pragma unroll
@@ -433,8 +457,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ copies
         uint32_t it = 0; // k blocks issued
         bool ok = true;
-        for (int i = pair; ok && get_tile<BN>(g, prefix, i, t); i += pairs) {
-            const int a_row = t.row + (int)rank * 128;
+        for (int i = pair; ok && get_tile<BN, kSwap, kMostTok>(g, prefix, i, t); i += pairs) {
+            const int a_row = t.row + (int)rank * 128; // kSwap: weight rows (columns of D) from n0
+            const int w_row = t.n0 + (int)rank * (g.gated ? 64 : 128), tok0 = t.row + (int)rank * (t.tok / 2);
+            const uint32_t bytes = kSwap ? C::kABytes + t.tok / 2 * 128u : C::kStage;
             const int b_row = g.gated ? (int)rank * g.n_cols + t.n0 : t.n0 + (int)rank * (BN / 2);
             for (int kb = 0; kb < t.nkb; ++kb, ++it) {
                 const int s = it % S;
@@ -450,18 +476,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     uint32_t bar = map_rank(full(s), 0);
                     if (cut) {
                         bar = map_rank(tail(s), rank);
-                        mbar_arrive_expect_tx(tail(s), C::kStage);
+                        mbar_arrive_expect_tx(tail(s), bytes);
                     } else {
-                        mbar_arrive_expect_tx_relaxed(bar, C::kStage);
+                        mbar_arrive_expect_tx_relaxed(bar, bytes);
                     }
                     const uint32_t sa = base + s * C::kStage, sb = sa + C::kABytes;
-                    if (kAMn) {
+                    if (kSwap) {
+                        if (kAMn) {
+                            for (int j = 0; j < 2; ++j)
+                                tma_pair_3d(sa + j * 8192, &map_a, w_row + j * 64, k, t.e, bar);
+                        } else if (g.gated) {
+                            tma_pair_5d(sa, &map_a, k, 0, 0, w_row / 16, t.e, bar);
+                        } else {
+                            tma_pair_3d(sa, &map_a, k, w_row, t.e, bar);
+                        }
+                        if (t.tok == 256)
+                            tma_pair_2d(sb, &map_b, k, tok0, bar);
+                        else
+                            for (int j = 0; j < t.tok / 32; ++j)
+                                tma_pair_2d(sb + j * 2048, &map_c, k, tok0 + j * 16, bar);
+                    } else if (kAMn) {
                         for (int j = 0; j < 2; ++j)
                             tma_pair_2d(sa + j * 8192, &map_a, a_row + j * 64, k, bar);
                     } else {
                         tma_pair_2d(sa, &map_a, k, a_row, bar);
                     }
-                    if (kBMn) {
+                    if (kSwap) {
+                    } else if (kBMn) {
                         for (int j = 0; j < BN / 128; ++j)
                             tma_pair_3d(sb + j * 8192, &map_b, b_row + j * 64, k, g.seg_k ? 0 : t.e, bar);
                     } else {
@@ -484,10 +525,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_wait_bounded(mma_done, 0, nullptr, kDrainNs); // the leader's last commit
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
-        const uint32_t idesc = idesc_f16(g.fmt, kAMn, kBMn, kTileM, BN);
         uint32_t it = 0, n = 0;
         bool ok = true;
-        for (int i = pair; ok && get_tile<BN>(g, prefix, i, t); i += pairs) {
+        for (int i = pair; ok && get_tile<BN, kSwap, kMostTok>(g, prefix, i, t); i += pairs) {
+            const uint32_t idesc = idesc_f16(g.fmt, kAMn, kBMn, kTileM, kSwap ? t.tok : BN);
             for (int kb = 0; ok && kb < t.nkb;) {
                 const int buf = n & 1;
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(acc_empty(buf), ((n >> 1) & 1) ^ 1, &g_linear_err, kWaitNs))) {
@@ -503,7 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    if (kAMn && t.rem && kb == t.nkb - 1)
+                    if (kAMn && kBMn && t.rem && kb == t.nkb - 1)
                         fence_acq_cluster(); // the other CTA's tail warp wrote its half by plain stores
                     tc_fence_after();
                     if (elect_lane()) {
@@ -533,7 +574,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (kAMn && kBMn && g.seg.E) {
             uint32_t it = 0, ph = 0; // ph: the phase of each stage's tail barrier
             bool ok = true;
-            for (int i = pair; ok && get_tile<BN>(g, prefix, i, t); i += pairs) {
+            for (int i = pair; ok && get_tile<BN, kSwap, kMostTok>(g, prefix, i, t); i += pairs) {
                 it += t.nkb;
                 if (!t.rem)
                     continue;
@@ -595,12 +636,124 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mbar_arrive_relaxed(map_rank(acc_empty(n & 1), 0)); // its TMEM reads are done (wait::ld)
             ++n;
         };
-        for (int i = pair; ok && get_tile<BN>(g, prefix, i, t); i += pairs) {
+        for (int i = pair; ok && get_tile<BN, kSwap, kMostTok>(g, prefix, i, t); i += pairs) {
             // gradients have no bias, preact, activation or residual
-            const Epi ep = kBMn ? Epi{nullptr, nullptr, g.out, nullptr, kActNone, g.N, g.n_cols, g.type, g.out_type, g.vec}
+            const Epi ep = kPlain ? Epi{nullptr, nullptr, g.out, nullptr, kActNone, g.N, g.n_cols, g.type, g.out_type, g.vec}
                                 : Epi{g.bias ? g.bias + (size_t)t.e * g.N : nullptr, g.residual, g.out, g.preact, g.act,
                                       g.N, g.n_cols, g.type, g.out_type, g.vec};
             const size_t d_off = g.seg_k ? (size_t)t.e * g.d_expert : (size_t)t.split * g.M * g.n_cols;
+            if constexpr (kSwap) {
+                // lane: a column of D; chunk c: tokens 32 c .. + 31, taken by the warp halves in turn
+                const bool gated = !kPlain && g.gated;
+                const uint32_t acc0 = (uint32_t)(q * 32) << 16;
+                // [token][column] through shared memory; groups of 4 columns change place by the token
+                // so that neither side meets bank conflicts
+                auto put = [&](const uint32_t (&r)[32]) {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        const int sw = (x & 1) | ((x & 2) << 1);
+                        stg[x * 32 + (((lane >> 2) ^ sw) << 2) + (lane & 3)] = __uint_as_float(r[x]);
+                    }
+                    __syncwarp();
+                };
+                auto get8 = [&](int token, int col, float (&f)[8]) {
+                    const int sw = (token & 1) | ((token & 2) << 1);
+                    const float4 *src = reinterpret_cast<const float4 *>(stg + token * 32);
+                    const float4 a = src[(col / 4) ^ sw], b = src[(col / 4 + 1) ^ sw];
+                    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+                    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+                };
+                Rows w;
+                Ahead<4> ahead;
+                Ahead<2> ahead2;
+                auto place = [&](int c) {
+                    // gated: 2 lanes to a token's 16 columns, tokens 16 apart; else 4 lanes to 32, 8 apart
+                    const int step = gated ? 16 : 8;
+                    const int m = t.row + c * 32 + (gated ? lane >> 1 : rl);
+                    w.n = gated ? t.n0 + (int)rank * 64 + q * 16 + (lane & 1) * 8 : t.n0 + (int)rank * 128 + q * 32 + c8;
+                    w.ok = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        w.ok |= m + j * step < t.row_end && w.n < g.n_cols ? 1u << j : 0u;
+                    w.so = step * g.n_cols, w.spo = step * g.N;
+                    w.o = d_off + (size_t)m * g.n_cols + w.n;
+                    w.po = (size_t)m * g.N + w.n;
+                    if (gated)
+                        ahead2.load(ep, w);
+                    else
+                        ahead.load(ep, w);
+                };
+                auto done = [&](const uint32_t (&r)[32]) {
+                    put(r);
+                    if (gated) {
+                        float v[2][8], up[2][8];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            get8(j * 16 + (lane >> 1), (lane & 1) * 8, v[j]);
+                            get8(j * 16 + (lane >> 1), 16 + (lane & 1) * 8, up[j]);
+                        }
+                        __syncwarp();
+                        finish<2, true>(ep, w, v, up, ahead2);
+                    } else {
+                        float v[4][8];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            get8(j * 8 + rl, c8, v[j]);
+                        __syncwarp();
+                        finish<4, false>(ep, w, v, v, ahead);
+                    }
+                };
+                const int chunks = t.tok / 32;
+                if constexpr (kSum) {
+                    uint32_t sum[2][32];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            sum[c][x] = 0u;
+                    for (int kb = 0; ok && kb < t.nkb; kb += kChain) {
+                        if (!wait_acc())
+                            break;
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            if (half + 2 * c < chunks) {
+                                uint32_t r[32];
+                                tmem_ld32(tmem + 256u * (n & 1) + acc0 + (half + 2 * c) * 32, r);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int x = 0; x < 32; ++x)
+                                    sum[c][x] = __float_as_uint(__uint_as_float(sum[c][x]) + __uint_as_float(r[x]));
+                            }
+                        free_acc();
+                    }
+                    if (!ok)
+                        break;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        if (half + 2 * c < chunks) {
+                            place(half + 2 * c);
+                            done(sum[c]);
+                        }
+                } else {
+                    if (half < chunks)
+                        place(half);
+                    if (!wait_acc())
+                        break;
+                    if (half >= chunks)
+                        free_acc();
+                    for (int c = half; c < chunks; c += 2) {
+                        if (c > half)
+                            place(c);
+                        uint32_t r[32];
+                        tmem_ld32(tmem + 256u * (n & 1) + acc0 + c * 32, r);
+                        tmem_wait_ld();
+                        if (c + 2 >= chunks)
+                            free_acc();
+                        done(r);
+                    }
+                }
+                continue;
+            }
             const int row0 = t.row + (int)rank * 128 + q * 32 + rl;
             Ahead<4> ahead;
             Rows w;
@@ -687,7 +840,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     float v[4][8] = {}, up[4][8] = {};
                     if (t.nkb > 0)
                         take(lc, v);
-                    if (!kBMn && g.gated) {
+                    if (!kPlain && g.gated) {
                         if (t.nkb > 0) {
                             take(BN / 2 + lc, up);
                             if (c + 32 >= cols)
@@ -791,52 +944,61 @@ void launch_pack(const void *src, void *dst, int64_t rows, int cols, cudaStream_
 // ---------------------------------------------------------------- launch
 constexpr int kPairs = 74; // SM pairs of the 148-SM part the plans are made for
 
-// Tile width and splits of a dense [M, cols] product over kb blocks of k, by the estimated cycles:
-// a 64-deep block of a 256 x BN tile takes about 256 + BN cycles (its MMAs 2 BN, its loads from L2
-// (16 KB + 64 BN bytes) / 64 a cycle), a tile about 1500 to start and finish, and a split product
-// writes and reads its float32 planes and launches a second kernel.
+// The shape of a dense [M, cols] product over kb blocks of k, by the estimated cycles: a 64-deep block of a
+// 256 x BN tile (BN weight rows, or BN tokens for kSwap) takes about 256 + BN cycles (its MMAs 2 BN,
+// its loads from L2 (16 KB + 64 BN bytes) / 64 a cycle), a tile about 1500 to start and finish, and
+// a split product writes and reads its float32 planes and launches a second kernel.
 struct Plan {
     int bn, splits;
-    bool sum; // the sum over chains of kChain k blocks kept in registers (at most 192 columns wide)
+    bool sum;  // the sum over chains of kChain k blocks kept in registers (at most 192 columns, or 128 tokens)
+    int tok;   // kSwap: tokens of a tile; else 0
 };
-Plan plan_dense(int64_t M, int cols, int kb, bool gated, bool mn, bool f32)
+Plan plan_dense(int64_t M, int cols, int kb, bool gated, bool mn, bool f32, bool swap)
 {
-    Plan best{256, 1, false};
-    if (kb == 0)
+    Plan best{256, 1, false, 0};
+    if (M == 0 || kb == 0)
         return best;
     double best_t = 1e30;
-    const int64_t mt = (M + kTileM - 1) / kTileM;
-    for (int bn : {256, 192, 128}) {
-        if (bn == 192 && (gated || mn)) // halves of 96 columns
-            continue;
-        for (int s = 1; s <= 16; ++s) {
-            if (s > 1 && kb / s < 4)
+    auto consider = [&](int bn, int tok, int64_t row_tiles, int col_tiles, int width) {
+        for (int s = 1; s <= 40; ++s) {
+            if (s > 1 && kb / s < 3)
                 break;
             const int64_t kbs = (kb + s - 1) / s;
+            if (s > 1 && kbs == (kb + s - 2) / (s - 1))
+                continue; // the same blocks a split as with one fewer
             const bool sum = f32 && kbs > kChain;
-            if (sum && bn == 256)
+            if (sum && width > (tok ? 128 : 192))
                 continue;
-            const int64_t tiles = mt * ((cols + bn - 1) / bn) * ((kb + kbs - 1) / kbs);
-            double t = (double)((tiles + kPairs - 1) / kPairs) * ((double)kbs * (256 + bn) + 1500);
+            const int64_t tiles = row_tiles * col_tiles * ((kb + kbs - 1) / kbs);
+            double t = (double)((tiles + kPairs - 1) / kPairs) * ((double)kbs * (256 + width) + 1500);
             if (s > 1)
                 t += 5000 + (double)s * M * cols * 8 / 4000;
             if (t < best_t)
-                best_t = t, best = Plan{bn, s, sum};
+                best_t = t, best = Plan{bn, s, sum, tok};
         }
-    }
+    };
+    for (int bn : {256, 192, 128})
+        if (bn != 192 || !(gated || mn)) // halves of 96 columns
+            consider(bn, 0, (M + kTileM - 1) / kTileM, (cols + bn - 1) / bn, bn);
+    if (swap)
+        for (int most : {256, 128}) {
+            const int64_t tiles = (M + most - 1) / most;
+            const int tok = (int)round_up((M + tiles - 1) / tiles, 32);
+            consider(256, tok, (M + tok - 1) / tok, (cols + 255) / 256, tok);
+        }
     return best;
 }
 
-template <int BN, bool kAMn, bool kBMn, bool kSum>
-int launch_gemm(const Gemm &g, const CUtensorMap &ma, const CUtensorMap &mb, int tiles, cudaStream_t s)
+template <int BN, bool kAMn, bool kBMn, bool kSum, bool kSwap = false>
+int launch_gemm(const Gemm &g, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mc, int tiles, cudaStream_t s)
 {
-    auto kernel = gemm_kernel<BN, kAMn, kBMn, kSum>;
+    auto kernel = gemm_kernel<BN, kAMn, kBMn, kSum, kSwap>;
     // per device and cheap; nothing to remember between calls
     cudaError_t ce = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::kSmem);
     if (ce != cudaSuccess)
         return cuda_fail(ce, "cudaFuncSetAttribute(linear)");
     const int pairs = tiles < kPairs ? tiles : kPairs;
-    ce = launch_kernel(kernel, dim3(2 * pairs), dim3(kThreads), Cfg<BN>::kSmem, s, true, g, ma, mb);
+    ce = launch_kernel(kernel, dim3(2 * pairs), dim3(kThreads), Cfg<BN>::kSmem, s, true, g, ma, mb, mc);
     return ce == cudaSuccess ? MOE_MX_OK : cuda_fail(ce, "linear product launch");
 }
 
@@ -867,14 +1029,40 @@ int run_gemm(Gemm &g, int bn, bool sum, const Operand &a, const Operand &b, int6
         return rc;
     if constexpr (!kBMn)
         if (sum)
-            return bn == 192 ? launch_gemm<192, kAMn, kBMn, true>(g, ma, mb, (int)tiles, s)
-                             : launch_gemm<128, kAMn, kBMn, true>(g, ma, mb, (int)tiles, s);
+            return bn == 192 ? launch_gemm<192, kAMn, kBMn, true>(g, ma, mb, mb, (int)tiles, s)
+                             : launch_gemm<128, kAMn, kBMn, true>(g, ma, mb, mb, (int)tiles, s);
     if (bn == 256)
-        return launch_gemm<256, kAMn, kBMn, false>(g, ma, mb, (int)tiles, s);
+        return launch_gemm<256, kAMn, kBMn, false>(g, ma, mb, mb, (int)tiles, s);
     if constexpr (!kBMn)
         if (bn == 192)
-            return launch_gemm<192, kAMn, kBMn, false>(g, ma, mb, (int)tiles, s);
-    return launch_gemm<128, kAMn, kBMn, false>(g, ma, mb, (int)tiles, s);
+            return launch_gemm<192, kAMn, kBMn, false>(g, ma, mb, mb, (int)tiles, s);
+    return launch_gemm<128, kAMn, kBMn, false>(g, ma, mb, mb, (int)tiles, s);
+}
+
+// The same with the weights as A: w rows (or, kWMn, its columns) and `tok` token rows of x.
+template <bool kWMn>
+int run_swap(Gemm &g, bool sum, const Operand &x, const Operand &w, int64_t tiles, cudaStream_t s)
+{
+    if (tiles > INT32_MAX)
+        return fail(MOE_MX_ERR_UNSUPPORTED, "the product has %lld tiles", (long long)tiles);
+    CUtensorMap ma, mb, mc;
+    int rc;
+    if (g.gated) {
+        // 16 gate rows, then the 16 up rows of the same columns, four times: lanes of one warp hold both
+        const cuuint64_t row = (cuuint64_t)w.ld * 2, half = (cuuint64_t)w.rows / 2;
+        const cuuint64_t dims[5] = {(cuuint64_t)w.inner, 16, 2, half / 16, (cuuint64_t)w.experts};
+        const cuuint64_t strides[4] = {row, row * half, row * 16, row * w.rows};
+        const cuuint32_t box[5] = {64, 16, 2, 4, 1};
+        rc = encode_nd(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, w.p, dims, strides, box);
+    } else {
+        rc = make_map(&ma, w, kWMn ? 64 : 128, true);
+    }
+    if (rc || (rc = make_map(&mb, x, 128, false)) || (rc = make_map(&mc, x, 16, false)))
+        return rc;
+    if constexpr (!kWMn)
+        if (sum)
+            return launch_gemm<256, kWMn, false, true, true>(g, ma, mb, mc, (int)tiles, s);
+    return launch_gemm<256, kWMn, false, false, true>(g, ma, mb, mc, (int)tiles, s);
 }
 
 // ---------------------------------------------------------------- dz and the bias gradient
@@ -1002,13 +1190,14 @@ ForwardPlan plan_linear(int E, int64_t M, int N, int K, int act, bool f32)
 {
     ForwardPlan f{};
     const bool gated = act == kActSwiglu;
+    const bool swap = !gated || N % 32 == 0; // gate and up rows are taken 16 by 16
     const int kb = (K + kBk - 1) / kBk;
     if (E == 0) {
         // a gated product is one of N columns in tiles of the gate's and the up's; a split one is plain
-        f.p = plan_dense(M, N, kb, gated, false, f32);
+        f.p = plan_dense(M, N, kb, gated, false, f32, swap);
     } else {
         const bool sum = f32 && kb > kChain;
-        f.p = Plan{N <= 128 || (sum && gated) ? 128 : sum ? 192 : 256, 1, sum};
+        f.p = Plan{swap ? 256 : 128, 1, sum, swap ? 256 : 0};
     }
     Parts ws;
     f.x = ws.take(K % 8 ? M * round_up(K, 8) * 2 : 0);
@@ -1020,22 +1209,29 @@ ForwardPlan plan_linear(int E, int64_t M, int N, int K, int act, bool f32)
 
 struct BackwardPlan {
     bool direct;
-    Plan dw;
+    Plan dx, dw;
     int64_t part, dz, x, w, planes, bytes;
 };
 BackwardPlan plan_backward(int E, int64_t M, int N, int K, int act, int type, int dout_type)
 {
     BackwardPlan f{};
     f.direct = dz_is_dout(act, type, dout_type, N);
-    f.dw = Plan{256, 1, false};
+    f.dx = Plan{256, 1, false, 256};
+    f.dw = Plan{256, 1, false, 0};
     if (E == 0)
-        f.dw = plan_dense(N, K, (int)((M + kBk - 1) / kBk), false, true, false);
+        f.dw = plan_dense(N, K, (int)((M + kBk - 1) / kBk), false, true, false, false);
+    if (E == 0 && M > 0) {
+        f.dx = plan_dense(M, K, (N + kBk - 1) / kBk, false, true, false, true);
+    }
     Parts ws;
     f.part = ws.take((M + 127) / 128 * N * 4);
     f.dz = ws.take(f.direct ? 0 : M * ldz_of(N) * 2);
     f.x = ws.take(K % 8 ? M * round_up(K, 8) * 2 : 0);
     f.w = ws.take(K % 8 ? (E ? E : 1) * (int64_t)N * round_up(K, 8) * 2 : 0);
-    f.planes = ws.take(f.dw.splits > 1 ? (int64_t)f.dw.splits * N * K * 4 : 0);
+    // dx's planes, then (dx is summed by then) dw's
+    const int64_t px = f.dx.splits > 1 ? f.dx.splits * M * K * 4 : 0;
+    const int64_t pw = f.dw.splits > 1 ? (int64_t)f.dw.splits * N * K * 4 : 0;
+    f.planes = ws.take(px > pw ? px : pw);
     f.bytes = ws.at;
     return f;
 }
@@ -1103,12 +1299,21 @@ int launch_linear(const LinearArgs &a, cudaStream_t s)
     const Epi ep = epilogue_of(g);
     const int kb = (a.K + kBk - 1) / kBk;
     split_out(g, f.p.splits, kb, a.N, ws + f.planes);
-    const int bn = g.gated ? f.p.bn / 2 : f.p.bn;
-    g.nt = (g.n_cols + bn - 1) / bn;
-    g.mt = (int)((a.M + kTileM - 1) / kTileM);
-    // grouped: every expert hit has at most one part-filled row tile
-    const int64_t mt = a.E ? a.M / kTileM + a.E : g.mt;
-    const int rc = run_gemm<false, false>(g, f.p.bn, f.p.sum, x, w, mt * g.nt * g.splits, s);
+    int rc;
+    if (f.p.tok) {
+        g.nt = (g.n_cols + (g.gated ? 127 : 255)) / (g.gated ? 128 : 256);
+        g.tok = f.p.tok;
+        g.mt = (int)((a.M + g.tok - 1) / g.tok);
+        const int most = f.p.sum ? 128 : 256; // grouped: every expert hit has at most one part-filled tile
+        const int64_t mt = a.E ? a.M / most + a.E : g.mt;
+        rc = run_swap<false>(g, f.p.sum, x, w, mt * g.nt * g.splits, s);
+    } else {
+        const int bn = g.gated ? f.p.bn / 2 : f.p.bn;
+        g.nt = (g.n_cols + bn - 1) / bn;
+        g.mt = (int)((a.M + kTileM - 1) / kTileM);
+        const int64_t mt = a.E ? a.M / kTileM + a.E : g.mt;
+        rc = run_gemm<false, false>(g, f.p.bn, f.p.sum, x, w, mt * g.nt * g.splits, s);
+    }
     if (rc || g.splits == 1)
         return rc;
     return launch_reduce(reinterpret_cast<float *>(ws + f.planes), g.splits, a.M, ep, s);
@@ -1157,12 +1362,22 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
         g.seg = seg, g.M = (int)a.M, g.n_cols = g.N = a.K, g.K = a.N;
         g.fmt = a.type == kTypeBf16, g.out = a.dx, g.type = g.out_type = a.type, g.vec = a.K % 8 == 0;
         const int kb = (a.N + kBk - 1) / kBk;
-        const int bn = a.K > 128 ? 256 : 128;
-        split_out(g, 1, kb, a.K, nullptr);
-        g.nt = (a.K + bn - 1) / bn;
-        g.mt = (int)((a.M + kTileM - 1) / kTileM);
-        const int64_t mt = a.E ? a.M / kTileM + a.E : g.mt;
-        if ((rc = run_gemm<false, true>(g, bn, false, oa, ob, mt * g.nt, s)))
+        const Epi ep = epilogue_of(g);
+        split_out(g, f.dx.splits, kb, a.K, ws + f.planes);
+        if (f.dx.tok) {
+            g.nt = (a.K + 255) / 256, g.tok = f.dx.tok;
+            g.mt = (int)((a.M + g.tok - 1) / g.tok);
+            const int64_t mt = a.E ? a.M / 256 + a.E : g.mt;
+            rc = run_swap<true>(g, false, oa, ob, mt * g.nt * g.splits, s);
+        } else {
+            const int bn = f.dx.bn;
+            g.nt = (a.K + bn - 1) / bn;
+            g.mt = (int)((a.M + kTileM - 1) / kTileM);
+            rc = run_gemm<false, true>(g, bn, false, oa, ob, (int64_t)g.mt * g.nt * g.splits, s);
+        }
+        if (rc)
+            return rc;
+        if (g.splits > 1 && (rc = launch_reduce(reinterpret_cast<float *>(ws + f.planes), g.splits, a.M, ep, s)))
             return rc;
     }
     if (a.dw) {

@@ -20,6 +20,7 @@ devices raise TypeError or ValueError before anything is enqueued.  Output buffe
 """
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple
 
 import torch
@@ -42,24 +43,28 @@ class Routing(NamedTuple):
     rows: int                  # rows of the grouped buffers
 
 
-def _tensor(t, name, like=None, dtype=None, shape=None):
+def _tensor(t, name, like, dtype=None, shape=None):
+    """t, checked: a contiguous tensor on the device of ``like``, of the given type and shape."""
+    # one test for the usual case: these checks are most of a small call's time on the host
+    if (isinstance(t, torch.Tensor) and (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)
+            and t.is_contiguous() and t.get_device() == like.get_device()):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} has type {t.dtype}, not {dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not {like.device}")
-    return t
+    raise ValueError(f"{name} is on {t.device}, not {like.device}")
 
 
 def _type(t, name):
-    if t.dtype not in _TYPES:
+    code = _TYPES.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name} has type {t.dtype}; bfloat16, float16 and float32 are supported")
-    return _TYPES[t.dtype]
+    return code
 
 
 def _on(t, stream):
@@ -67,29 +72,62 @@ def _on(t, stream):
     if not t.is_cuda:
         raise ValueError(f"tensors must be on a CUDA device, not {t.device}")
     if stream is None:
-        return torch.cuda.current_stream(t.device).cuda_stream
+        return _raw_stream(t.get_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+# The current stream's handle without a Stream object around it (2 us less a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _empty(shape, dtype, like, stream):
     """A new tensor that the call's stream uses first (the allocator learns of a stream of its own)."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
+    t = like.new_empty(shape, dtype=dtype)
     if isinstance(stream, torch.cuda.Stream):
         t.record_stream(stream)
     return t
 
 
 def _pairs(r: Routing, like):
-    T, k = r.topk_w.shape
+    shape = r.topk_w.shape
     _tensor(r.topk_w, "topk_w", like, torch.float32)
+    if len(shape) != 2:
+        raise ValueError("topk_w must be [tokens, slots]")
+    T, k = shape
     _tensor(r.pos_of_pair, "pos_of_pair", like, torch.int32, (T * k,))
     return T, k
+
+
+def _matrix(t, name, like, rows=None, dtype=None):
+    """t as a checked [rows, columns] matrix; its columns."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not [{'rows' if rows is None else rows}, columns]")
+    _tensor(t, name, like, dtype)
+    return t.shape[1]
 
 
 def _out(out, shape, dtype, like, name, stream):
     if out is None:
         return _empty(shape, dtype, like, stream)
     return _tensor(out, name, like, dtype, shape)
+
+
+def _call(name, *args):
+    """The entry point of that name on raw arguments; raises MoeMxError."""
+    code = getattr(moe_mx.load_library(), name)(*args)
+    if code:
+        raise moe_mx.MoeMxError(code, moe_mx.moe_mx_last_error())
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+_linear_workspace = functools.lru_cache(1024)(moe_mx.moe_mx_linear_workspace)  # by sizes and types alone
+_linear_backward_workspace = functools.lru_cache(1024)(moe_mx.moe_mx_linear_backward_workspace)
 
 
 def max_grouped_rows(pairs: int, num_experts: int) -> int:
@@ -101,10 +139,8 @@ def max_grouped_rows(pairs: int, num_experts: int) -> int:
 def route_group(router_logits: torch.Tensor, top_k: int, stream=None) -> Routing:
     """Softmax top-k routing of float32 logits [T, E] and the grouped layout of the pairs
     (moe_mx_route_group_noalloc, whose calls on one device share a scratch: order them)."""
-    _tensor(router_logits, "router_logits", dtype=torch.float32)
-    if router_logits.dim() != 2:
-        raise ValueError("router_logits must be [tokens, experts]")
-    T, E = router_logits.shape
+    E = _matrix(router_logits, "router_logits", router_logits, dtype=torch.float32)
+    T = router_logits.shape[0]
     on = _on(router_logits, stream)
     rows = max_grouped_rows(T * top_k, E)
     new = lambda *shape, dtype=torch.int32: _empty(shape, dtype, router_logits, stream)  # noqa: E731
@@ -121,22 +157,25 @@ def route_group(router_logits: torch.Tensor, top_k: int, stream=None) -> Routing
 def dispatch(x: torch.Tensor, routing: Routing, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Token rows x [T, H] at their pairs' grouped rows: [rows, H]; padding rows are not written."""
     T, k = _pairs(routing, x)
-    _tensor(x, "x", shape=(T, x.shape[-1]))
+    H = _matrix(x, "x", x, T)
     on = _on(x, stream)
-    out = _out(out, (routing.rows, x.shape[1]), x.dtype, x, "out", stream)
-    moe_mx.moe_mx_dispatch(x, T, x.shape[1], k, routing.pos_of_pair, routing.rows, _type(x, "x"), out, on)
+    code = _type(x, "x")
+    out = _out(out, (routing.rows, H), x.dtype, x, "out", stream)
+    _call("moe_mx_dispatch", x.data_ptr(), T, H, k, routing.pos_of_pair.data_ptr(), routing.rows, code, out.data_ptr(),
+          on)
     return out
 
 
 def _combine(grouped, routing, w, out_dtype, out, stream):
     T, k = _pairs(routing, grouped)
-    _tensor(grouped, "grouped", shape=(routing.rows, grouped.shape[-1]))
+    H = _matrix(grouped, "grouped", grouped, routing.rows)
     on = _on(grouped, stream)
     if out is not None:
         out_dtype = out.dtype
-    out = _out(out, (T, grouped.shape[1]), out_dtype or grouped.dtype, grouped, "out", stream)
-    moe_mx.moe_mx_combine(grouped, routing.rows, T, grouped.shape[1], k, routing.pos_of_pair, w,
-                          _type(grouped, "grouped"), _type(out, "out"), out, on)
+    code = _type(grouped, "grouped")
+    out = _out(out, (T, H), out_dtype or grouped.dtype, grouped, "out", stream)
+    _call("moe_mx_combine", grouped.data_ptr(), routing.rows, T, H, k, routing.pos_of_pair.data_ptr(), _ptr(w), code,
+          _type(out, "out"), out.data_ptr(), on)
     return out
 
 
@@ -157,48 +196,49 @@ def combine_backward(dout: torch.Tensor, grouped: torch.Tensor, routing: Routing
     """Gradient of combine: (dgrouped [rows, H], dtopk_w [T, k], dlogits [T, num_experts] or None when
     num_experts is 0).  dlogits is the gradient through the router's softmax over the chosen logits."""
     T, k = _pairs(routing, dout)
-    H = dout.shape[-1]
-    _tensor(dout, "dout", shape=(T, H))
+    H = _matrix(dout, "dout", dout, T)
     _tensor(grouped, "grouped", dout, shape=(routing.rows, H))
     on = _on(dout, stream)
+    code, dout_code = _type(grouped, "grouped"), _type(dout, "dout")
     dy = _out(dy, (routing.rows, H), grouped.dtype, dout, "dy", stream)
     dw = _empty((T, k), torch.float32, dout, stream)
-    dlogits = None
+    ids = dlogits = None
     if num_experts:
-        _tensor(routing.topk_ids, "topk_ids", dout, torch.int32, (T, k))
+        ids = _tensor(routing.topk_ids, "topk_ids", dout, torch.int32, (T, k))
         dlogits = _empty((T, num_experts), torch.float32, dout, stream)
-    moe_mx.moe_mx_combine_backward(dout, grouped, routing.rows, T, H, k, routing.pos_of_pair, routing.topk_w,
-                                   routing.topk_ids, num_experts, _type(grouped, "grouped"), _type(dout, "dout"), dy,
-                                   dw, dlogits, on)
+    _call("moe_mx_combine_backward", dout.data_ptr(), grouped.data_ptr(), routing.rows, T, H, k,
+          routing.pos_of_pair.data_ptr(), routing.topk_w.data_ptr(), _ptr(ids), num_experts, code, dout_code,
+          dy.data_ptr(), dw.data_ptr(), _ptr(dlogits), on)
     return dy, dw, dlogits
 
 
 def _linear_sizes(x, w, activation, routing):
-    """(experts, rows, N, K, activation, columns of out) of a linear call, its operands checked."""
-    if activation not in ACTIVATIONS:
+    """(experts, rows, N, K, activation, columns of out, counts, pad_offsets) of a linear call, its operands
+    checked; raw pointers for the last two."""
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation {activation!r} is not one of {', '.join(ACTIVATIONS)}")
-    _tensor(x, "x")
-    _tensor(w, "w", x, x.dtype)
-    if x.dtype not in (torch.bfloat16, torch.float16):
+    K = _matrix(x, "x", x)
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float16:
         raise TypeError(f"x has type {x.dtype}; bfloat16 and float16 are supported")
+    _tensor(w, "w", x, x.dtype)
     E = 0 if routing is None else routing.counts.shape[0]
-    if x.dim() != 2 or w.dim() != (3 if E else 2) or w.shape[-1] != x.shape[1] or (E and w.shape[0] != E):
+    if w.dim() != (3 if E else 2) or w.shape[-1] != K or (E and w.shape[0] != E):
         raise ValueError(f"x {tuple(x.shape)} and w {tuple(w.shape)}: need [rows, K] and "
                          + (f"[{E}, N, K]" if E else "[N, K]"))
-    rows, K = x.shape
-    N = w.shape[-2]
+    rows, N = x.shape[0], w.shape[-2]
+    counts = pad = None
     if E:
         if rows != routing.rows:
             raise ValueError(f"x has {rows} rows, the grouped layout {routing.rows}")
-        _tensor(routing.counts, "counts", x, torch.int32, (E,))
-        _tensor(routing.pad_offsets, "pad_offsets", x, torch.int32, (E + 1,))
-    if activation == "swiglu" and N % 2:
-        raise ValueError(f"swiglu needs an even number of weight rows, not {N}")
-    return E, rows, N, K, ACTIVATIONS[activation], N // 2 if activation == "swiglu" else N
-
-
-def _segments(routing):
-    return (None, None) if routing is None else (routing.counts, routing.pad_offsets)
+        counts = _tensor(routing.counts, "counts", x, torch.int32, (E,)).data_ptr()
+        pad = _tensor(routing.pad_offsets, "pad_offsets", x, torch.int32, (E + 1,)).data_ptr()
+    cols = N
+    if activation == "swiglu":
+        if N % 2:
+            raise ValueError(f"swiglu needs an even number of weight rows, not {N}")
+        cols = N // 2
+    return E, rows, N, K, act, cols, counts, pad
 
 
 def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
@@ -209,7 +249,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
     rows are grouped, w [E, N, K] and bias [E, N].  out and residual: [rows, N] ([rows, N/2] for
     swiglu) of x's type or float32; residual may be out itself.  A ``preact`` buffer [rows, N] receives
     x w^T + bias for linear_backward."""
-    E, rows, N, K, act, cols = _linear_sizes(x, w, activation, routing)
+    E, rows, N, K, act, cols, counts, pad = _linear_sizes(x, w, activation, routing)
     on = _on(x, stream)
     if bias is not None:
         _tensor(bias, "bias", x, torch.float32, (E, N) if E else (N,))
@@ -223,10 +263,10 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
     if preact is not None:
         _tensor(preact, "preact", x, x.dtype, (rows, N))
     dt, ot = _type(x, "x"), _type(out, "out")
-    need = moe_mx.moe_mx_linear_workspace(E, rows, N, K, dt, act, ot)
+    need = _linear_workspace(E, rows, N, K, dt, act, ot)
     ws = _empty(need, torch.uint8, x, stream) if need else None
-    moe_mx.moe_mx_linear(x, w, bias, residual, *_segments(routing), E, rows, N, K, dt, act, ot, out, preact, ws, need,
-                         on)
+    _call("moe_mx_linear", x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), counts, pad, E, rows, N, K, dt, act,
+          ot, out.data_ptr(), _ptr(preact), _ptr(ws), need, on)
     return out
 
 
@@ -236,21 +276,21 @@ def linear_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, preact
                     dw: torch.Tensor | None = None, stream=None):
     """Gradient of linear: (dx, dw, dbias), None for those not asked for.  dout is of x's type or float32;
     preact as linear wrote it (for an activation).  The residual's gradient is dout."""
-    E, rows, N, K, act, cols = _linear_sizes(x, w, activation, routing)
+    E, rows, N, K, act, cols, counts, pad = _linear_sizes(x, w, activation, routing)
     on = _on(x, stream)
     _tensor(dout, "dout", x, shape=(rows, cols))
-    if activation != "none":
+    if act:
         _tensor(preact, "preact", x, x.dtype, (rows, N))
     elif preact is not None:
         raise ValueError("preact is taken with an activation only")
     if not (input_grad or weight_grad or bias_grad):
         raise ValueError("no gradient is asked for")
-    dx = _out(dx, (rows, K), x.dtype, x, "dx", stream) if input_grad else None
-    dw = _out(dw, tuple(w.shape), x.dtype, x, "dw", stream) if weight_grad else None
-    db = _empty((E, N) if E else (N,), torch.float32, x, stream) if bias_grad else None
     dt, gt = _type(x, "x"), _type(dout, "dout")
-    need = moe_mx.moe_mx_linear_backward_workspace(E, rows, N, K, dt, act, gt)
+    dx = _out(dx, (rows, K), x.dtype, x, "dx", stream) if input_grad else None
+    dw = _out(dw, w.shape, x.dtype, x, "dw", stream) if weight_grad else None
+    db = _empty((E, N) if E else (N,), torch.float32, x, stream) if bias_grad else None
+    need = _linear_backward_workspace(E, rows, N, K, dt, act, gt)
     ws = _empty(need, torch.uint8, x, stream) if need else None
-    moe_mx.moe_mx_linear_backward(dout, x, w, preact, *_segments(routing), E, rows, N, K, dt, act, gt, dx, dw, db, ws,
-                                  need, on)
+    _call("moe_mx_linear_backward", dout.data_ptr(), x.data_ptr(), w.data_ptr(), _ptr(preact), counts, pad, E, rows, N,
+          K, dt, act, gt, _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), need, on)
     return dx, dw, db
