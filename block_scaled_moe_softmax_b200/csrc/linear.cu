@@ -376,10 +376,14 @@ constexpr int kChain = 8;
 
 __device__ uint32_t g_linear_err; // set by a wait that gave up
 
+struct TokenMaps { // token rows in boxes of 16, 32 and 64 rows
+    CUtensorMap m[3];
+};
+
 template <int BN, bool kAMn, bool kBMn, bool kSum, bool kSwap>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_kernel(const Gemm g, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                const __grid_constant__ CUtensorMap map_c)
+                const __grid_constant__ TokenMaps map_c)
 {
     using C = Cfg<BN>;
     constexpr bool kPlain = kSwap ? kAMn : kBMn;  // a gradient: no bias, preact, activation or residual
@@ -413,8 +417,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_mbar_init();
         prefetch_tensormap(&map_a);
         prefetch_tensormap(&map_b);
-        if (kSwap)
-            prefetch_tensormap(&map_c);
     }
     if (warp == 2)
         tmem_alloc_pair(tmem_slot, 512);
@@ -460,7 +462,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = pair; ok && get_tile<BN, kSwap, kMostTok>(g, prefix, i, t); i += pairs) {
             const int a_row = t.row + (int)rank * 128; // kSwap: weight rows (columns of D) from n0
             const int w_row = t.n0 + (int)rank * (g.gated ? 64 : 128), tok0 = t.row + (int)rank * (t.tok / 2);
-            const uint32_t bytes = kSwap ? C::kABytes + t.tok / 2 * 128u : C::kStage;
+            // kSwap: one box of 16, 32, 64 or 128 token rows, the least that holds the tile's half (a copy
+            // of exactly its rows, 16 at a time, costs more in copies issued than it saves in bytes:
+            // 0.54 against 0.37 us a k block at 224 tokens)
+            const int box_log = t.tok > 128 ? 3 : t.tok > 64 ? 2 : t.tok > 32 ? 1 : 0;
+            const uint32_t bytes = kSwap ? C::kABytes + (2048u << box_log) : C::kStage;
             const int b_row = g.gated ? (int)rank * g.n_cols + t.n0 : t.n0 + (int)rank * (BN / 2);
             for (int kb = 0; kb < t.nkb; ++kb, ++it) {
                 const int s = it % S;
@@ -490,11 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         } else {
                             tma_pair_3d(sa, &map_a, k, w_row, t.e, bar);
                         }
-                        if (t.tok == 256)
-                            tma_pair_2d(sb, &map_b, k, tok0, bar);
-                        else
-                            for (int j = 0; j < t.tok / 32; ++j)
-                                tma_pair_2d(sb + j * 2048, &map_c, k, tok0 + j * 16, bar);
+                        tma_pair_2d(sb, box_log == 3 ? &map_b : &map_c.m[box_log], k, tok0, bar);
                     } else if (kAMn) {
                         for (int j = 0; j < 2; ++j)
                             tma_pair_2d(sa + j * 8192, &map_a, a_row + j * 64, k, bar);
@@ -990,7 +992,7 @@ Plan plan_dense(int64_t M, int cols, int kb, bool gated, bool mn, bool f32, bool
 }
 
 template <int BN, bool kAMn, bool kBMn, bool kSum, bool kSwap = false>
-int launch_gemm(const Gemm &g, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mc, int tiles, cudaStream_t s)
+int launch_gemm(const Gemm &g, const CUtensorMap &ma, const CUtensorMap &mb, const TokenMaps &mc, int tiles, cudaStream_t s)
 {
     auto kernel = gemm_kernel<BN, kAMn, kBMn, kSum, kSwap>;
     // per device and cheap; nothing to remember between calls
@@ -1029,14 +1031,14 @@ int run_gemm(Gemm &g, int bn, bool sum, const Operand &a, const Operand &b, int6
         return rc;
     if constexpr (!kBMn)
         if (sum)
-            return bn == 192 ? launch_gemm<192, kAMn, kBMn, true>(g, ma, mb, mb, (int)tiles, s)
-                             : launch_gemm<128, kAMn, kBMn, true>(g, ma, mb, mb, (int)tiles, s);
+            return bn == 192 ? launch_gemm<192, kAMn, kBMn, true>(g, ma, mb, TokenMaps{}, (int)tiles, s)
+                             : launch_gemm<128, kAMn, kBMn, true>(g, ma, mb, TokenMaps{}, (int)tiles, s);
     if (bn == 256)
-        return launch_gemm<256, kAMn, kBMn, false>(g, ma, mb, mb, (int)tiles, s);
+        return launch_gemm<256, kAMn, kBMn, false>(g, ma, mb, TokenMaps{}, (int)tiles, s);
     if constexpr (!kBMn)
         if (bn == 192)
-            return launch_gemm<192, kAMn, kBMn, false>(g, ma, mb, mb, (int)tiles, s);
-    return launch_gemm<128, kAMn, kBMn, false>(g, ma, mb, mb, (int)tiles, s);
+            return launch_gemm<192, kAMn, kBMn, false>(g, ma, mb, TokenMaps{}, (int)tiles, s);
+    return launch_gemm<128, kAMn, kBMn, false>(g, ma, mb, TokenMaps{}, (int)tiles, s);
 }
 
 // The same with the weights as A: w rows (or, kWMn, its columns) and `tok` token rows of x.
@@ -1045,7 +1047,8 @@ int run_swap(Gemm &g, bool sum, const Operand &x, const Operand &w, int64_t tile
 {
     if (tiles > INT32_MAX)
         return fail(MOE_MX_ERR_UNSUPPORTED, "the product has %lld tiles", (long long)tiles);
-    CUtensorMap ma, mb, mc;
+    CUtensorMap ma, mb;
+    TokenMaps mc;
     int rc;
     if (g.gated) {
         // 16 gate rows, then the 16 up rows of the same columns, four times: lanes of one warp hold both
@@ -1057,7 +1060,8 @@ int run_swap(Gemm &g, bool sum, const Operand &x, const Operand &w, int64_t tile
     } else {
         rc = make_map(&ma, w, kWMn ? 64 : 128, true);
     }
-    if (rc || (rc = make_map(&mb, x, 128, false)) || (rc = make_map(&mc, x, 16, false)))
+    if (rc || (rc = make_map(&mb, x, 128, false)) || (rc = make_map(&mc.m[0], x, 16, false)) ||
+        (rc = make_map(&mc.m[1], x, 32, false)) || (rc = make_map(&mc.m[2], x, 64, false)))
         return rc;
     if constexpr (!kWMn)
         if (sum)
