@@ -828,6 +828,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             } else {
+                if (kPlain && g.vec && g.out_type != kTypeF32 && cols % 64 == 0) {
+                    // A gradient: rounded where it lies (lane: row), turned 64 columns at a time as 16-bit
+                    // values, stored as whole 128-byte lines.  Half the shared-memory traffic of float32
+                    // blocks of 32 columns; gradients have short k, and this is what bounds them.
+                    if (t.nkb > 0 && !wait_acc())
+                        break;
+                    uint4 *const line = reinterpret_cast<uint4 *>(stg);
+                    uint16_t *const out = static_cast<uint16_t *>(g.out) + d_off;
+                    const int r8 = lane >> 3, l8 = lane & 7;
+                    for (int c = 0; c < cols; c += 64) {
+                        const int lc = half * cols + c;
+                        uint32_t r0[32] = {}, r1[32] = {};
+                        if (t.nkb > 0) {
+                            tmem_ld32(tmem + 256u * (n & 1) + lanes + lc, r0);
+                            tmem_ld32(tmem + 256u * (n & 1) + lanes + lc + 32, r1);
+                            tmem_wait_ld();
+                            if (c + 64 >= cols)
+                                free_acc();
+                        }
+                        auto pack = [&](auto zero) {
+                            using T = decltype(zero);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t a[4], b[4];
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    a[x] = pack2(__uint_as_float(r0[8 * j + 2 * x]), __uint_as_float(r0[8 * j + 2 * x + 1]), T());
+                                    b[x] = pack2(__uint_as_float(r1[8 * j + 2 * x]), __uint_as_float(r1[8 * j + 2 * x + 1]), T());
+                                }
+                                line[lane * 8 + (j ^ (lane & 7))] = make_uint4(a[0], a[1], a[2], a[3]);
+                                line[lane * 8 + ((j + 4) ^ (lane & 7))] = make_uint4(b[0], b[1], b[2], b[3]);
+                            }
+                        };
+                        if (g.type == kTypeF16)
+                            pack(__half());
+                        else
+                            pack(__nv_bfloat16());
+                        __syncwarp();
+                        const int nn = t.n0 + lc + l8 * 8;
+                        uint4 v[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            v[j] = line[(j * 4 + r8) * 8 + (l8 ^ ((j * 4 + r8) & 7))];
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int m = t.row + (int)rank * 128 + q * 32 + j * 4 + r8;
+                            if (m < t.row_end && nn < g.n_cols)
+                                *reinterpret_cast<uint4 *>(out + (size_t)m * g.n_cols + nn) = v[j];
+                        }
+                    }
+                    continue;
+                }
                 auto take = [&](uint32_t col, float (&f)[4][8]) {
                     uint32_t r[32];
                     tmem_ld32(tmem + 256u * (n & 1) + lanes + col, r);
@@ -962,12 +1015,10 @@ Plan plan_dense(int64_t M, int cols, int kb, bool gated, bool mn, bool f32, bool
         return best;
     double best_t = 1e30;
     auto consider = [&](int bn, int tok, int64_t row_tiles, int col_tiles, int width) {
-        for (int s = 1; s <= 40; ++s) {
+        for (int s : {1, 2, 3, 4, 6, 8, 12, 18, 24, 36}) {
             if (s > 1 && kb / s < 3)
                 break;
             const int64_t kbs = (kb + s - 1) / s;
-            if (s > 1 && kbs == (kb + s - 2) / (s - 1))
-                continue; // the same blocks a split as with one fewer
             const bool sum = f32 && kbs > kChain;
             if (sum && width > (tok ? 128 : 192))
                 continue;
@@ -989,6 +1040,194 @@ Plan plan_dense(int64_t M, int cols, int kb, bool gated, bool mn, bool f32, bool
             consider(256, tok, (M + tok - 1) / tok, (cols + 255) / 256, tok);
         }
     return best;
+}
+
+// ---------------------------------------------------------------- a few rows
+// Up to 16 rows of x (one decode step): the product streams w once and its time is w's bytes over the
+// memory rate, or launch latency.  Weight rows are the A operand of 16 x 8 x 16 warp MMAs, tokens the
+// B operand; a warp takes kR x 16 weight rows over a slice of k, the 8 warps of a CTA and the CTAs of a
+// cluster share k, and the partial sums meet in shared memory (a fixed order, one launch, where
+// a split tile product writes planes and launches a second kernel: 16.7 -> 10 us a call of
+// 384 x 7168, most of it the host's).  Within a 32-element k block lane t of a row's four holds elements
+// 8t .. 8t + 7 of both operands (one 16-byte load), which the two MMAs take in the same order.
+constexpr int kSmallRows = 16, kSmallWarps = 8, kMaxCluster = 8;
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    if constexpr (sizeof(T) == sizeof(__half) && !__is_same(T, __nv_bfloat16))
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+struct SmallArgs {
+    const void *x, *w;
+    int M, N, K, k_warp; // k_warp: elements of k of one warp (a multiple of 32)
+    Epi epi;
+};
+
+// kR: 16-row weight tiles of a CTA (swiglu: a gate and an up tile); kNb: 8-token groups.
+template <typename T, int kR, int kNb, bool kGated>
+__global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(const SmallArgs a)
+{
+    constexpr int kOut = kR * 16 * kNb * 8; // partial sums of a CTA: [weight row][token]
+    __shared__ float part[kSmallWarps][kOut];
+    __shared__ float total[kOut];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    uint32_t ranks, rank = cluster_rank();
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
+    const int tile = blockIdx.x / ranks;
+    const int n0 = tile * (kGated ? 16 : kR * 16); // first column of D
+    const int cols = a.epi.n_cols;
+    const T *w = static_cast<const T *>(a.w), *x = static_cast<const T *>(a.x);
+    const T *wp[2 * kR], *xp[kNb];
+    bool wok[2 * kR], xok[kNb];
+#pragma unroll
+    for (int r = 0; r < 2 * kR; ++r) {
+        const int n = kGated ? n0 + (r & 1) * 8 + g : n0 + r * 8 + g;
+        wok[r] = n < cols;
+        wp[r] = w + (size_t)(wok[r] ? n + (kGated && r >= 2 ? cols : 0) : 0) * a.K + 8 * t;
+    }
+#pragma unroll
+    for (int b = 0; b < kNb; ++b) {
+        xok[b] = b * 8 + g < a.M;
+        xp[b] = x + (size_t)(xok[b] ? b * 8 + g : 0) * a.K + 8 * t;
+    }
+    float acc[kR][kNb][4] = {};
+    const int k0 = (int)(rank * kSmallWarps + warp) * a.k_warp, k1 = min(a.K, k0 + a.k_warp);
+    constexpr int kU = 4; // k blocks of 32 in flight
+    for (int k = k0; k < k1; k += 32 * kU) {
+        uint4 wv[kU][2 * kR], xv[kU][kNb];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int ku = k + 32 * u;
+            const bool in = ku + 8 * t < k1; // K is a multiple of 8: 8 elements are in or out together
+#pragma unroll
+            for (int r = 0; r < 2 * kR; ++r)
+                wv[u][r] = in && wok[r] ? __ldcs(reinterpret_cast<const uint4 *>(wp[r] + ku)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int b = 0; b < kNb; ++b)
+                xv[u][b] = in && xok[b] ? __ldg(reinterpret_cast<const uint4 *>(xp[b] + ku)) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int r = 0; r < kR; ++r)
+#pragma unroll
+                for (int b = 0; b < kNb; ++b) {
+                    const uint4 lo = wv[u][2 * r], hi = wv[u][2 * r + 1], v = xv[u][b];
+                    mma16816<T>(acc[r][b], lo.x, hi.x, lo.y, hi.y, v.x, v.y);
+                    mma16816<T>(acc[r][b], lo.z, hi.z, lo.w, hi.w, v.z, v.w);
+                }
+    }
+    // element (weight row 16 r + g (+ 8), token 8 b + 2 t (+ 1))
+#pragma unroll
+    for (int r = 0; r < kR; ++r)
+#pragma unroll
+        for (int b = 0; b < kNb; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                part[warp][(r * 16 + g + (i >> 1) * 8) * (kNb * 8) + b * 8 + 2 * t + (i & 1)] = acc[r][b][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < kOut; i += kSmallWarps * 32) {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < kSmallWarps; ++j)
+            s += part[j][i];
+        total[i] = s;
+    }
+    if (ranks > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (rank == 0) {
+        const Epi &e = a.epi;
+        for (int i = threadIdx.x; i < (kGated ? kOut / 2 : kOut); i += kSmallWarps * 32) {
+            // neighbouring threads: neighbouring columns of one token
+            const int rows = kGated ? 16 : kR * 16, c = i % rows, m = i / rows, n = n0 + c;
+            if (m >= a.M || n >= cols)
+                continue;
+            float z = 0.f, up = 0.f;
+            for (uint32_t q = 0; q < ranks; ++q) {
+                z += load_rank(&total[c * (kNb * 8) + m], q);
+                if (kGated)
+                    up += load_rank(&total[(16 + c) * (kNb * 8) + m], q);
+            }
+            if (e.bias) {
+                z += __ldg(e.bias + n);
+                if (kGated)
+                    up += __ldg(e.bias + cols + n);
+            }
+            if (e.preact) {
+                T *p = static_cast<T *>(e.preact) + (size_t)m * e.N + n;
+                *p = from_f32<T>(z);
+                if (kGated)
+                    p[cols] = from_f32<T>(up);
+            }
+            float v = kGated ? z * sigmoid(z) * up : act_fwd(z, e.act);
+            const size_t o = (size_t)m * cols + n;
+            if (e.out_type == kTypeF32) {
+                if (e.residual)
+                    v += static_cast<const float *>(e.residual)[o];
+                static_cast<float *>(e.out)[o] = v;
+            } else {
+                if (e.residual)
+                    v += to_f32<T>(static_cast<const T *>(e.residual)[o]);
+                static_cast<T *>(e.out)[o] = from_f32<T>(v);
+            }
+        }
+    }
+    if (ranks > 1)
+        cluster_sync(); // the other CTAs' shared memory is read until here
+}
+
+// Whether a dense product runs as small_kernel: up to 16 rows, and rows of w of whole 16 bytes.
+bool is_small(int64_t M, int K) { return M <= kSmallRows && K % 8 == 0; }
+
+int launch_small(const SmallArgs &args, int type, cudaStream_t s)
+{
+    SmallArgs a = args;
+    const bool gated = a.epi.act == kActSwiglu;
+    // 32 weight rows a CTA halve the reads of x; 16 where that leaves SMs without a CTA
+    const bool two = gated || a.N >= 32 * 296;
+    const int tiles = (a.epi.n_cols + (two && !gated ? 31 : 15)) / (two && !gated ? 32 : 16);
+    // k is shared by as many CTAs of a cluster as two CTAs to each SM take, each warp keeping 64 elements
+    int ranks = 1;
+    while (ranks < kMaxCluster && tiles * ranks * 2 <= 2 * 2 * kPairs * 2 && a.K >= 64 * kSmallWarps * ranks * 2)
+        ranks *= 2;
+    a.k_warp = (int)round_up((a.K + kSmallWarps * ranks - 1) / (kSmallWarps * ranks), 32);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tiles * ranks);
+    cfg.blockDim = dim3(kSmallWarps * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t ce = cudaSuccess;
+    by_half(type, [&](auto zero) {
+        using T = decltype(zero);
+        const bool one = a.M <= 8;
+        if (gated)
+            ce = cudaLaunchKernelEx(&cfg, one ? small_kernel<T, 2, 1, true> : small_kernel<T, 2, 2, true>, a);
+        else if (two)
+            ce = cudaLaunchKernelEx(&cfg, one ? small_kernel<T, 2, 1, false> : small_kernel<T, 2, 2, false>, a);
+        else
+            ce = cudaLaunchKernelEx(&cfg, one ? small_kernel<T, 1, 1, false> : small_kernel<T, 1, 2, false>, a);
+    });
+    return ce == cudaSuccess ? MOE_MX_OK : cuda_fail(ce, "linear launch");
 }
 
 template <int BN, bool kAMn, bool kBMn, bool kSum, bool kSwap = false>
@@ -1060,9 +1299,13 @@ int run_swap(Gemm &g, bool sum, const Operand &x, const Operand &w, int64_t tile
     } else {
         rc = make_map(&ma, w, kWMn ? 64 : 128, true);
     }
-    if (rc || (rc = make_map(&mb, x, 128, false)) || (rc = make_map(&mc.m[0], x, 16, false)) ||
-        (rc = make_map(&mc.m[1], x, 32, false)) || (rc = make_map(&mc.m[2], x, 64, false)))
+    // the boxes that the tiles may use: a dense product's are tiles of g.tok tokens, and a shorter last one
+    const int most = g.seg.E ? 256 : g.tok;
+    if (rc || (rc = make_map(&mb, x, most > 128 ? 128 : 16, false)))
         return rc;
+    for (int i = 0; i < 3; ++i)
+        if ((i == 0 || most > 16 << i) && (rc = make_map(&mc.m[i], x, 16 << i, false)))
+            return rc;
     if constexpr (!kWMn)
         if (sum)
             return launch_gemm<256, kWMn, false, true, true>(g, ma, mb, mc, (int)tiles, s);
@@ -1086,44 +1329,58 @@ template <typename T, typename TO, int V> __global__ void __launch_bounds__(256)
     const int64_t m0 = (int64_t)blockIdx.x * 128;
     int e;
     int64_t end;
+    grid_dep_wait();
+    grid_dep_launch();
     const bool any = find_segment(a.seg, m0, e, end);
     if (!any)
         return; // a block of padding, or past the last segment
     const bool gated = a.act == kActSwiglu;
     const int cl = threadIdx.x % 8, rl = threadIdx.x / 8;
     float sum[2][8] = {};
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + i * 32 + rl;
-        if (m >= end)
-            continue;
-        for (int v = 0; v < 8; v += V) {
-            const int n = blockIdx.y * 64 + cl * 8 + v;
-            if (n >= a.n_out)
-                break;
-            Raw<TO, V> rd;
-            Raw<T, V> rz;
-            float d[V], z[V], u[V], dz[V], du[V];
-            rd.load(static_cast<const TO *>(a.dout) + m * a.n_out + n);
-            rd.get(d);
-            if (a.act != kActNone) {
-                rz.load(static_cast<const T *>(a.preact) + m * a.N + n);
-                rz.get(z);
-            }
-            if (gated) {
-                rz.load(static_cast<const T *>(a.preact) + m * a.N + n + a.n_out);
-                rz.get(u);
-            }
+    for (int v = 0; v < 8; v += V) {
+        const int n = blockIdx.y * 64 + cl * 8 + v;
+        if (n >= a.n_out)
+            break;
+        // the loads of all four rows before the first use
+        Raw<TO, V> rd[4];
+        Raw<T, V> rz[4], ru[4];
 #pragma unroll
-            for (int q = 0; q < V; ++q) {
-                if (gated) {
+        for (int i = 0; i < 4; ++i) {
+            const int64_t m = m0 + i * 32 + rl;
+            if (m >= end)
+                continue;
+            rd[i].load(static_cast<const TO *>(a.dout) + m * a.n_out + n);
+            if (a.act != kActNone)
+                rz[i].load(static_cast<const T *>(a.preact) + m * a.N + n);
+            if (gated)
+                ru[i].load(static_cast<const T *>(a.preact) + m * a.N + n + a.n_out);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t m = m0 + i * 32 + rl;
+            if (m >= end)
+                continue;
+            float d[V], z[V], u[V], dz[V], du[V];
+            rd[i].get(d);
+            if (gated) {
+                rz[i].get(z);
+                ru[i].get(u);
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
                     const float sg = sigmoid(z[q]);
                     dz[q] = d[q] * u[q] * (sg * (1.f + z[q] * (1.f - sg)));
                     du[q] = d[q] * z[q] * sg;
+                    sum[0][v + q] += dz[q];
                     sum[1][v + q] += du[q];
-                } else {
-                    dz[q] = a.act == kActNone ? d[q] : d[q] * act_grad(z[q], a.act);
                 }
-                sum[0][v + q] += dz[q];
+            } else {
+                if (a.act != kActNone)
+                    rz[i].get(z);
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
+                    dz[q] = a.act == kActNone ? d[q] : d[q] * act_grad(z[q], a.act);
+                    sum[0][v + q] += dz[q];
+                }
             }
             if (a.dz) {
                 T *o = static_cast<T *>(a.dz) + m * a.ldz + n;
@@ -1155,6 +1412,8 @@ template <typename T, typename TO, int V> __global__ void __launch_bounds__(256)
 // dbias[e][n]: the sum of the segment's row blocks, in order.
 __global__ void __launch_bounds__(256) dbias_kernel(const float *part, Segments seg, int N, float *dbias)
 {
+    grid_dep_wait(); // the blocks' sums
+    grid_dep_launch();
     const int n = blockIdx.x * blockDim.x + threadIdx.x, e = blockIdx.y;
     if (n >= N)
         return;
@@ -1193,6 +1452,8 @@ struct ForwardPlan {
 ForwardPlan plan_linear(int E, int64_t M, int N, int K, int act, bool f32)
 {
     ForwardPlan f{};
+    if (E == 0 && is_small(M, K))
+        return f;
     const bool gated = act == kActSwiglu;
     const bool swap = !gated || N % 32 == 0; // gate and up rows are taken 16 by 16
     const int kb = (K + kBk - 1) / kBk;
@@ -1289,6 +1550,11 @@ int64_t linear_backward_workspace(int E, int64_t M, int N, int K, int act, int t
 
 int launch_linear(const LinearArgs &a, cudaStream_t s)
 {
+    if (a.E == 0 && is_small(a.M, a.K)) {
+        const SmallArgs m{a.x, a.w, (int)a.M, a.N, a.K, 0,
+                          Epi{a.bias, a.residual, a.out, a.preact, a.act, a.N, a.No(), a.type, a.out_type, 0}};
+        return launch_small(m, a.type, s);
+    }
     const ForwardPlan f = plan_linear(a.E, a.M, a.N, a.K, a.act, a.out_type == kTypeF32);
     char *ws = static_cast<char *>(a.ws);
     const int ld = (int)round_up(a.K, 8), experts = a.E ? a.E : 1;
@@ -1341,10 +1607,7 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
             using T = decltype(x);
             auto go = [&](auto y) {
                 using TO = decltype(y);
-                if (d.n_out % 8 == 0)
-                    dz_kernel<T, TO, 8><<<grid, 256, 0, s>>>(d);
-                else
-                    dz_kernel<T, TO, 1><<<grid, 256, 0, s>>>(d);
+                launch_kernel(d.n_out % 8 == 0 ? dz_kernel<T, TO, 8> : dz_kernel<T, TO, 1>, grid, dim3(256), 0, s, true, d);
             };
             if (a.dout_type == kTypeF32)
                 go(float());
@@ -1354,7 +1617,7 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
     }
     if (a.dbias) {
         const dim3 grid((a.N + 255) / 256, a.E ? a.E : 1);
-        dbias_kernel<<<grid, 256, 0, s>>>(part, seg, a.N, a.dbias);
+        launch_kernel(dbias_kernel, grid, dim3(256), 0, s, true, (const float *)part, seg, a.N, a.dbias);
     }
     const void *dz = f.direct ? a.dout : d.dz;
     const int ldz = f.direct ? a.N : d.ldz, ldk = (int)round_up(a.K, 8), experts = a.E ? a.E : 1;

@@ -36,6 +36,14 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank)
     return r;
 }
 
+// A float of the same shared variable in the CTA of rank `rank`.
+__device__ __forceinline__ float load_rank(const float *p, uint32_t rank)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_rank(smem_u32(p), rank)) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
