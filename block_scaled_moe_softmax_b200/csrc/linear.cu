@@ -130,14 +130,17 @@ constexpr int kTileM = 256, kBk = 64, kMaxSeg = kMaxExperts;
 constexpr int kThreads = 384, kEpiWarps = 8;
 constexpr unsigned long long kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
 
-template <int BN> struct Cfg {
+template <int BN, bool kSwap> struct Cfg {
     static constexpr int kABytes = 128 * kBk * 2, kBBytes = BN / 2 * kBk * 2, kStage = kABytes + kBBytes;
-    static constexpr int kStages = BN == 256 ? 5 : BN == 192 ? 6 : 7;
+    // BN = 256: the experts' tile counts take the sixth stage's room where rows are segmented
+    static constexpr bool kPrefix = kSwap || BN == 128;
+    static constexpr int kStages = BN == 256 ? (kPrefix ? 5 : 6) : BN == 192 ? 6 : 7;
     static constexpr int kOffEpi = kStages * kStage, kOffBar = kOffEpi + kEpiWarps * 4096;
-    // barriers: full, empty, tail per stage, 2 acc_full, 2 acc_empty, mma_done; then the TMEM address
-    static constexpr int kNumBar = 3 * kStages + 5;
+    // barriers: full, empty per stage, 2 acc_full, 2 acc_empty, mma_done; then the TMEM address
+    static constexpr int kNumBar = 2 * kStages + 5;
     static constexpr int kOffPrefix = kOffBar + kNumBar * 8 + 8;
-    static constexpr int kSmem = kOffPrefix + (kMaxSeg + 1) * 4 + 1024; // + alignment of the base
+    static constexpr int kSmem = kOffPrefix + (kPrefix ? (kMaxSeg + 1) * 4 : 0) + 1024; // + alignment of the base
+    static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
 
 struct Tile {
@@ -376,16 +379,18 @@ constexpr int kChain = 8;
 
 __device__ uint32_t g_linear_err; // set by a wait that gave up
 
-struct TokenMaps { // token rows in boxes of 16, 32 and 64 rows
+// kSwap: token rows in boxes of 16, 32 and 64 rows.  dw of grouped rows: each expert's last k block of
+// A and of B with zeros behind its rows, 64 rows an expert (cut_kernel).
+struct MoreMaps {
     CUtensorMap m[3];
 };
 
 template <int BN, bool kAMn, bool kBMn, bool kSum, bool kSwap>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_kernel(const Gemm g, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                const __grid_constant__ TokenMaps map_c)
+                const __grid_constant__ MoreMaps map_c)
 {
-    using C = Cfg<BN>;
+    using C = Cfg<BN, kSwap>;
     constexpr bool kPlain = kSwap ? kAMn : kBMn;  // a gradient: no bias, preact, activation or residual
     constexpr int kMostTok = kSum ? 128 : 256;    // kSwap: tokens of a tile (kSum keeps them in registers)
     extern __shared__ uint8_t smem_raw[];
@@ -397,17 +402,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t bar0 = base + C::kOffBar;
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (S + s); };
-    auto tail = [&](int s) { return bar0 + 8u * (2 * S + s); };
-    auto acc_full = [&](int b) { return bar0 + 8u * (3 * S + b); };
-    auto acc_empty = [&](int b) { return bar0 + 8u * (3 * S + 2 + b); };
-    const uint32_t mma_done = bar0 + 8u * (3 * S + 4), tmem_slot = bar0 + 8u * C::kNumBar;
-    int32_t *const prefix = reinterpret_cast<int32_t *>(sm + C::kOffPrefix);
+    auto acc_full = [&](int b) { return bar0 + 8u * (2 * S + b); };
+    auto acc_empty = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
+    const uint32_t mma_done = bar0 + 8u * (2 * S + 4), tmem_slot = bar0 + 8u * C::kNumBar;
+    int32_t *const prefix = reinterpret_cast<int32_t *>(sm + C::kOffPrefix); // kPrefix only
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(full(s), 2);  // each CTA's copies (or its tail warp)
+            mbar_init(full(s), 2);  // each CTA's copies
             mbar_init(empty(s), 1); // the commit of the MMAs that read the stage
-            mbar_init(tail(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full(b), 1);
@@ -422,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_alloc_pair(tmem_slot, 512);
     grid_dep_wait(); // everything this kernel reads, and the buffers it writes
     grid_dep_launch();
-    if (warp == 3 && g.seg.E && !g.seg_k) {
+    if (C::kPrefix && warp == 3 && g.seg.E && !g.seg_k) {
         int run = 0;
         for (int e0 = 0; e0 < g.seg.E; e0 += 32) {
             const int e = e0 + lane;
@@ -476,16 +479,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) {
                     const int k = t.k0 + kb * kBk;
-                    // the last block of a segment inside the rows: this CTA's tail warp clears the rows
-                    // behind the segment before the leader may use the block
-                    const bool cut = t.rem && kb == t.nkb - 1;
-                    uint32_t bar = map_rank(full(s), 0);
-                    if (cut) {
-                        bar = map_rank(tail(s), rank);
-                        mbar_arrive_expect_tx(tail(s), bytes);
-                    } else {
-                        mbar_arrive_expect_tx_relaxed(bar, bytes);
-                    }
+                    const uint32_t bar = map_rank(full(s), 0);
+                    mbar_arrive_expect_tx_relaxed(bar, bytes);
+                    // the last block of a segment whose rows end inside it: its copy filled up with zeros
+                    const bool cut = kAMn && kBMn && t.rem && kb == t.nkb - 1;
+                    const int kr = cut ? t.e * kBk : k;
                     const uint32_t sa = base + s * C::kStage, sb = sa + C::kABytes;
                     if (kSwap) {
                         if (kAMn) {
@@ -499,14 +497,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tma_pair_2d(sb, box_log == 3 ? &map_b : &map_c.m[box_log], k, tok0, bar);
                     } else if (kAMn) {
                         for (int j = 0; j < 2; ++j)
-                            tma_pair_2d(sa + j * 8192, &map_a, a_row + j * 64, k, bar);
+                            tma_pair_2d(sa + j * 8192, cut ? &map_c.m[0] : &map_a, a_row + j * 64, kr, bar);
                     } else {
                         tma_pair_2d(sa, &map_a, k, a_row, bar);
                     }
                     if (kSwap) {
                     } else if (kBMn) {
                         for (int j = 0; j < BN / 128; ++j)
-                            tma_pair_3d(sb + j * 8192, &map_b, b_row + j * 64, k, g.seg_k ? 0 : t.e, bar);
+                            tma_pair_3d(sb + j * 8192, cut ? &map_c.m[1] : &map_b, b_row + j * 64, kr, g.seg_k ? 0 : t.e, bar);
                     } else {
                         tma_pair_3d(sb, &map_b, k, b_row, t.e, bar);
                     }
@@ -546,8 +544,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    if (kAMn && kBMn && t.rem && kb == t.nkb - 1)
-                        fence_acq_cluster(); // the other CTA's tail warp wrote its half by plain stores
                     tc_fence_after();
                     if (elect_lane()) {
                         const uint32_t sa = base + s * C::kStage, sb = sa + C::kABytes;
@@ -571,33 +567,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             umma_commit_pair(mma_done);
         __syncwarp();
         mbar_wait_bounded(mma_done, 0, nullptr, kDrainNs);
-    } else if (warp == 2) {
-        // ------------------------------------------------------------ cut k blocks
-        if (kAMn && kBMn && g.seg.E) {
-            uint32_t it = 0, ph = 0; // ph: the phase of each stage's tail barrier
-            bool ok = true;
-            for (int i = pair; ok && get_tile<BN, kSwap, kMostTok>(g, prefix, i, t); i += pairs) {
-                it += t.nkb;
-                if (!t.rem)
-                    continue;
-                const int s = (it - 1) % S;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(tail(s), (ph >> s) & 1, &g_linear_err, kWaitNs))) {
-                    ok = false;
-                    break;
-                }
-                ph ^= 1u << s;
-                // rows (of k) behind the segment, in each box of 64 rows x 128 bytes
-                uint8_t *const st = sm + s * C::kStage;
-                for (int b = 0; b < C::kStage / 8192; ++b)
-                    for (int r = t.rem * 8 + lane; r < 64 * 8; r += 32)
-                        reinterpret_cast<uint4 *>(st + b * 8192)[r] = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_cluster(map_rank(full(s), 0));
-                __syncwarp();
-            }
-        }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3, half = (warp - 4) >> 2;
@@ -996,6 +965,32 @@ void launch_pack(const void *src, void *dst, int64_t rows, int cols, cudaStream_
                                                                  (int)round_up(cols, 8));
 }
 
+// dw of grouped rows takes a segment in 64-row blocks of k.  The last one's rows behind the segment are
+// padding, which may hold anything, so that block of dz and of x is copied with zeros behind its rows
+// (clearing it in shared memory instead held every tile up by about a microsecond).
+struct CutArgs {
+    const uint16_t *src[2]; // dz, x
+    uint16_t *dst[2];       // [E][64][ld]
+    int ld[2];              // elements per row, multiples of 8
+    Segments seg;
+};
+__global__ void __launch_bounds__(256) cut_kernel(const CutArgs a)
+{
+    grid_dep_wait();
+    grid_dep_launch();
+    const int e = blockIdx.x, o = blockIdx.z;
+    int first;
+    const int rows = segment_rows(a.seg, e, first), rem = rows % kBk;
+    if (rem == 0)
+        return;
+    const uint16_t *src = a.src[o] + (size_t)(first + rows - rem) * a.ld[o];
+    uint16_t *dst = a.dst[o] + (size_t)e * kBk * a.ld[o];
+    for (int r = blockIdx.y; r < kBk; r += gridDim.y)
+        for (int c = threadIdx.x * 8; c < a.ld[o]; c += 256 * 8)
+            *reinterpret_cast<uint4 *>(dst + (size_t)r * a.ld[o] + c) =
+                r < rem ? *reinterpret_cast<const uint4 *>(src + (size_t)r * a.ld[o] + c) : make_uint4(0, 0, 0, 0);
+}
+
 // ---------------------------------------------------------------- launch
 constexpr int kPairs = 74; // SM pairs of the 148-SM part the plans are made for
 
@@ -1231,15 +1226,15 @@ int launch_small(const SmallArgs &args, int type, cudaStream_t s)
 }
 
 template <int BN, bool kAMn, bool kBMn, bool kSum, bool kSwap = false>
-int launch_gemm(const Gemm &g, const CUtensorMap &ma, const CUtensorMap &mb, const TokenMaps &mc, int tiles, cudaStream_t s)
+int launch_gemm(const Gemm &g, const CUtensorMap &ma, const CUtensorMap &mb, const MoreMaps &mc, int tiles, cudaStream_t s)
 {
     auto kernel = gemm_kernel<BN, kAMn, kBMn, kSum, kSwap>;
     // per device and cheap; nothing to remember between calls
-    cudaError_t ce = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::kSmem);
+    cudaError_t ce = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN, kSwap>::kSmem);
     if (ce != cudaSuccess)
         return cuda_fail(ce, "cudaFuncSetAttribute(linear)");
     const int pairs = tiles < kPairs ? tiles : kPairs;
-    ce = launch_kernel(kernel, dim3(2 * pairs), dim3(kThreads), Cfg<BN>::kSmem, s, true, g, ma, mb, mc);
+    ce = launch_kernel(kernel, dim3(2 * pairs), dim3(kThreads), Cfg<BN, kSwap>::kSmem, s, true, g, ma, mb, mc);
     return ce == cudaSuccess ? MOE_MX_OK : cuda_fail(ce, "linear product launch");
 }
 
@@ -1260,7 +1255,8 @@ int make_map(CUtensorMap *map, const Operand &o, int box_rows, bool three)
 
 // tiles: an upper bound of the product's tiles (the kernel finds a grouped product's on the device)
 template <bool kAMn, bool kBMn>
-int run_gemm(Gemm &g, int bn, bool sum, const Operand &a, const Operand &b, int64_t tiles, cudaStream_t s)
+int run_gemm(Gemm &g, int bn, bool sum, const Operand &a, const Operand &b, int64_t tiles, cudaStream_t s,
+             const MoreMaps &more = MoreMaps{})
 {
     if (tiles > INT32_MAX)
         return fail(MOE_MX_ERR_UNSUPPORTED, "the product has %lld tiles", (long long)tiles);
@@ -1270,14 +1266,14 @@ int run_gemm(Gemm &g, int bn, bool sum, const Operand &a, const Operand &b, int6
         return rc;
     if constexpr (!kBMn)
         if (sum)
-            return bn == 192 ? launch_gemm<192, kAMn, kBMn, true>(g, ma, mb, TokenMaps{}, (int)tiles, s)
-                             : launch_gemm<128, kAMn, kBMn, true>(g, ma, mb, TokenMaps{}, (int)tiles, s);
+            return bn == 192 ? launch_gemm<192, kAMn, kBMn, true>(g, ma, mb, more, (int)tiles, s)
+                             : launch_gemm<128, kAMn, kBMn, true>(g, ma, mb, more, (int)tiles, s);
     if (bn == 256)
-        return launch_gemm<256, kAMn, kBMn, false>(g, ma, mb, TokenMaps{}, (int)tiles, s);
+        return launch_gemm<256, kAMn, kBMn, false>(g, ma, mb, more, (int)tiles, s);
     if constexpr (!kBMn)
         if (bn == 192)
-            return launch_gemm<192, kAMn, kBMn, false>(g, ma, mb, TokenMaps{}, (int)tiles, s);
-    return launch_gemm<128, kAMn, kBMn, false>(g, ma, mb, TokenMaps{}, (int)tiles, s);
+            return launch_gemm<192, kAMn, kBMn, false>(g, ma, mb, more, (int)tiles, s);
+    return launch_gemm<128, kAMn, kBMn, false>(g, ma, mb, more, (int)tiles, s);
 }
 
 // The same with the weights as A: w rows (or, kWMn, its columns) and `tok` token rows of x.
@@ -1287,7 +1283,7 @@ int run_swap(Gemm &g, bool sum, const Operand &x, const Operand &w, int64_t tile
     if (tiles > INT32_MAX)
         return fail(MOE_MX_ERR_UNSUPPORTED, "the product has %lld tiles", (long long)tiles);
     CUtensorMap ma, mb;
-    TokenMaps mc;
+    MoreMaps mc;
     int rc;
     if (g.gated) {
         // 16 gate rows, then the 16 up rows of the same columns, four times: lanes of one warp hold both
@@ -1475,7 +1471,7 @@ ForwardPlan plan_linear(int E, int64_t M, int N, int K, int act, bool f32)
 struct BackwardPlan {
     bool direct;
     Plan dx, dw;
-    int64_t part, dz, x, w, planes, bytes;
+    int64_t part, dz, x, w, planes, cut_a, cut_b, bytes;
 };
 BackwardPlan plan_backward(int E, int64_t M, int N, int K, int act, int type, int dout_type)
 {
@@ -1497,6 +1493,8 @@ BackwardPlan plan_backward(int E, int64_t M, int N, int K, int act, int type, in
     const int64_t px = f.dx.splits > 1 ? f.dx.splits * M * K * 4 : 0;
     const int64_t pw = f.dw.splits > 1 ? (int64_t)f.dw.splits * N * K * 4 : 0;
     f.planes = ws.take(px > pw ? px : pw);
+    f.cut_a = ws.take((int64_t)E * kBk * ldz_of(N) * 2);
+    f.cut_b = ws.take((int64_t)E * kBk * round_up(K, 8) * 2);
     f.bytes = ws.at;
     return f;
 }
@@ -1664,7 +1662,21 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
             g.seg_k = 0; // one segment: k ends with the rows, where the copies read zeros
         g.nt = (a.K + f.dw.bn - 1) / f.dw.bn;
         g.mt = (a.N + kTileM - 1) / kTileM;
-        if ((rc = run_gemm<true, true>(g, f.dw.bn, false, oa, ob, (int64_t)g.mt * g.nt * (a.E ? a.E : g.splits), s)))
+        MoreMaps more{};
+        if (a.E) {
+            CutArgs c{};
+            c.seg = seg;
+            c.src[0] = static_cast<const uint16_t *>(dz), c.src[1] = static_cast<const uint16_t *>(ob.p);
+            c.dst[0] = reinterpret_cast<uint16_t *>(ws + f.cut_a), c.dst[1] = reinterpret_cast<uint16_t *>(ws + f.cut_b);
+            c.ld[0] = ldz, c.ld[1] = ldk;
+            const cudaError_t ce = launch_kernel(cut_kernel, dim3(a.E, a.E < 64 ? 16 : 4, 2), dim3(256), 0, s, true, c);
+            if (ce != cudaSuccess)
+                return cuda_fail(ce, "cut_kernel launch");
+            const Operand ca{c.dst[0], a.N, (int64_t)a.E * kBk, ldz, 1}, cb{c.dst[1], a.K, (int64_t)a.E * kBk, ldk, 1};
+            if ((rc = make_map(&more.m[0], ca, 64, false)) || (rc = make_map(&more.m[1], cb, 64, true)))
+                return rc;
+        }
+        if ((rc = run_gemm<true, true>(g, f.dw.bn, false, oa, ob, (int64_t)g.mt * g.nt * (a.E ? a.E : g.splits), s, more)))
             return rc;
         if (g.splits > 1)
             return launch_reduce(reinterpret_cast<float *>(ws + f.planes), g.splits, a.N, ep, s);

@@ -44,11 +44,6 @@ __device__ __forceinline__ float load_rank(const float *p, uint32_t rank)
     return v;
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
 // Arrivals that order none of the thread's memory accesses: for barriers that guard asynchronous copies
 // (whose bytes the barrier counts itself) or TMEM.  A release at cluster scope waits for the thread's
 // earlier copies to land: measured, it held the copies to one k block (about 1500 cycles) at a time.
@@ -61,13 +56,6 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_relaxed(uint32_t bar, uint
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// Orders what another CTA of the cluster released by an arrival that this thread has seen before this
-// thread's later operations.
-__device__ __forceinline__ void fence_acq_cluster()
-{
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 
 // TMA loads into this CTA's shared memory whose bytes are counted on `bar`, a barrier of either CTA
