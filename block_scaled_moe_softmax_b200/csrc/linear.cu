@@ -380,7 +380,7 @@ constexpr int kChain = 8;
 __device__ uint32_t g_linear_err; // set by a wait that gave up
 
 // kSwap: token rows in boxes of 16, 32 and 64 rows.  dw of grouped rows: each expert's last k block of
-// A and of B with zeros behind its rows, 64 rows an expert (cut_kernel).
+// A and of B with zeros behind its rows, 64 rows an expert (after_kernel).
 struct MoreMaps {
     CUtensorMap m[3];
 };
@@ -965,32 +965,6 @@ void launch_pack(const void *src, void *dst, int64_t rows, int cols, cudaStream_
                                                                  (int)round_up(cols, 8));
 }
 
-// dw of grouped rows takes a segment in 64-row blocks of k.  The last one's rows behind the segment are
-// padding, which may hold anything, so that block of dz and of x is copied with zeros behind its rows
-// (clearing it in shared memory instead held every tile up by about a microsecond).
-struct CutArgs {
-    const uint16_t *src[2]; // dz, x
-    uint16_t *dst[2];       // [E][64][ld]
-    int ld[2];              // elements per row, multiples of 8
-    Segments seg;
-};
-__global__ void __launch_bounds__(256) cut_kernel(const CutArgs a)
-{
-    grid_dep_wait();
-    grid_dep_launch();
-    const int e = blockIdx.x, o = blockIdx.z;
-    int first;
-    const int rows = segment_rows(a.seg, e, first), rem = rows % kBk;
-    if (rem == 0)
-        return;
-    const uint16_t *src = a.src[o] + (size_t)(first + rows - rem) * a.ld[o];
-    uint16_t *dst = a.dst[o] + (size_t)e * kBk * a.ld[o];
-    for (int r = blockIdx.y; r < kBk; r += gridDim.y)
-        for (int c = threadIdx.x * 8; c < a.ld[o]; c += 256 * 8)
-            *reinterpret_cast<uint4 *>(dst + (size_t)r * a.ld[o] + c) =
-                r < rem ? *reinterpret_cast<const uint4 *>(src + (size_t)r * a.ld[o] + c) : make_uint4(0, 0, 0, 0);
-}
-
 // ---------------------------------------------------------------- launch
 constexpr int kPairs = 74; // SM pairs of the 148-SM part the plans are made for
 
@@ -1405,24 +1379,59 @@ template <typename T, typename TO, int V> __global__ void __launch_bounds__(256)
     }
 }
 
-// dbias[e][n]: the sum of the segment's row blocks, in order.
-__global__ void __launch_bounds__(256) dbias_kernel(const float *part, Segments seg, int N, float *dbias)
+// What a gradient needs of dz beside the products, in one launch.
+//
+// dbias[e][n]: the sum of the segment's 128-row blocks, 4 threads to a column, in a fixed order.
+//
+// Last k blocks: dw of grouped rows takes a segment in 64-row blocks of k.  The last one's rows behind the
+// segment are padding, which may hold anything, so that block of dz and of x is copied with zeros
+// behind its rows (clearing it in shared memory instead held every tile up by about a microsecond).
+struct AfterArgs {
+    const float *part;
+    float *dbias;           // nullptr: none
+    int N, bias_blocks;     // CTAs of dbias: columns / 64 per expert
+    const uint16_t *src[2]; // dz, x; nullptr: no copies
+    uint16_t *dst[2];       // [E][64][ld]
+    int ld[2];              // elements per row, multiples of 8
+    Segments seg;
+};
+
+constexpr int kCutRows = 4; // rows of a copy that one CTA takes
+
+__global__ void __launch_bounds__(256) after_kernel(const AfterArgs a)
 {
-    grid_dep_wait(); // the blocks' sums
+    grid_dep_wait(); // dz and its blocks' sums
     grid_dep_launch();
-    const int n = blockIdx.x * blockDim.x + threadIdx.x, e = blockIdx.y;
-    if (n >= N)
+    __shared__ float s[4][64];
+    const int e = blockIdx.y;
+    int first = 0;
+    const int64_t rows = a.seg.E ? segment_rows(a.seg, e, first) : a.seg.M;
+    if ((int)blockIdx.x < a.bias_blocks) {
+        const int c = threadIdx.x & 63, g = threadIdx.x >> 6, n = blockIdx.x * 64 + c;
+        const int64_t blocks = (rows + 127) / 128;
+        float t = 0.f;
+        if (n < a.N) {
+            const float *p = a.part + (size_t)(first / 128) * a.N + n;
+#pragma unroll 4
+            for (int64_t b = g; b < blocks; b += 4)
+                t += p[b * a.N];
+        }
+        s[g][c] = t;
+        __syncthreads();
+        if (g == 0 && n < a.N)
+            a.dbias[(size_t)e * a.N + n] = (s[0][c] + s[1][c]) + (s[2][c] + s[3][c]);
         return;
-    int64_t b0 = 0, rows = seg.M;
-    if (seg.E) {
-        int first;
-        rows = segment_rows(seg, e, first);
-        b0 = first / 128;
     }
-    float t = 0.f;
-    for (int64_t b = 0; b * 128 < rows; ++b)
-        t += part[(b0 + b) * N + n];
-    dbias[(size_t)e * N + n] = t;
+    const int rem = (int)(rows % kBk);
+    if (rem == 0)
+        return;
+    const int i = blockIdx.x - a.bias_blocks, o = i & 1, r0 = (i >> 1) * kCutRows;
+    const uint16_t *src = a.src[o] + (size_t)(first + rows - rem) * a.ld[o];
+    uint16_t *dst = a.dst[o] + (size_t)e * kBk * a.ld[o];
+    for (int r = r0; r < r0 + kCutRows; ++r)
+        for (int c = threadIdx.x * 8; c < a.ld[o]; c += 256 * 8)
+            *reinterpret_cast<uint4 *>(dst + (size_t)r * a.ld[o] + c) =
+                r < rem ? *reinterpret_cast<const uint4 *>(src + (size_t)r * a.ld[o] + c) : make_uint4(0, 0, 0, 0);
 }
 
 int ldz_of(int N) { return (int)round_up(N, 8); }
@@ -1613,12 +1622,24 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
                 go(T());
         });
     }
-    if (a.dbias) {
-        const dim3 grid((a.N + 255) / 256, a.E ? a.E : 1);
-        launch_kernel(dbias_kernel, grid, dim3(256), 0, s, true, (const float *)part, seg, a.N, a.dbias);
-    }
     const void *dz = f.direct ? a.dout : d.dz;
     const int ldz = f.direct ? a.N : d.ldz, ldk = (int)round_up(a.K, 8), experts = a.E ? a.E : 1;
+    const void *xk = a.dw && a.M > 0 ? packed(a.x, a.M, a.K, ws, f.x, s) : nullptr; // x with aligned rows
+    const bool cut = a.dw && a.E && a.M > 0;
+    if (a.dbias || cut) {
+        AfterArgs p{};
+        p.seg = seg, p.part = part, p.dbias = a.dbias, p.N = a.N;
+        p.bias_blocks = a.dbias ? (a.N + 63) / 64 : 0;
+        if (cut) {
+            p.src[0] = static_cast<const uint16_t *>(dz), p.src[1] = static_cast<const uint16_t *>(xk);
+            p.dst[0] = reinterpret_cast<uint16_t *>(ws + f.cut_a), p.dst[1] = reinterpret_cast<uint16_t *>(ws + f.cut_b);
+            p.ld[0] = ldz, p.ld[1] = ldk;
+        }
+        const dim3 grid(p.bias_blocks + (cut ? 2 * kBk / kCutRows : 0), experts);
+        const cudaError_t ce = launch_kernel(after_kernel, grid, dim3(256), 0, s, true, p);
+        if (ce != cudaSuccess)
+            return cuda_fail(ce, "bias gradient launch");
+    }
     int rc;
     if (a.dx && a.M > 0) {
         const Operand oa{dz, a.N, a.M, ldz, 1};
@@ -1651,7 +1672,7 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
             return ce == cudaSuccess ? MOE_MX_OK : cuda_fail(ce, "cudaMemsetAsync(dw)");
         }
         const Operand oa{dz, a.N, a.M, ldz, 1};
-        const Operand ob{packed(a.x, a.M, a.K, ws, f.x, s), a.K, a.M, ldk, 1};
+        const Operand ob{xk, a.K, a.M, ldk, 1};
         Gemm g{};
         g.seg = seg, g.seg_k = 1, g.M = a.N, g.n_cols = g.N = a.K, g.K = (int)a.M;
         g.d_expert = (int64_t)a.N * a.K;
@@ -1664,15 +1685,7 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
         g.mt = (a.N + kTileM - 1) / kTileM;
         MoreMaps more{};
         if (a.E) {
-            CutArgs c{};
-            c.seg = seg;
-            c.src[0] = static_cast<const uint16_t *>(dz), c.src[1] = static_cast<const uint16_t *>(ob.p);
-            c.dst[0] = reinterpret_cast<uint16_t *>(ws + f.cut_a), c.dst[1] = reinterpret_cast<uint16_t *>(ws + f.cut_b);
-            c.ld[0] = ldz, c.ld[1] = ldk;
-            const cudaError_t ce = launch_kernel(cut_kernel, dim3(a.E, a.E < 64 ? 16 : 4, 2), dim3(256), 0, s, true, c);
-            if (ce != cudaSuccess)
-                return cuda_fail(ce, "cut_kernel launch");
-            const Operand ca{c.dst[0], a.N, (int64_t)a.E * kBk, ldz, 1}, cb{c.dst[1], a.K, (int64_t)a.E * kBk, ldk, 1};
+            const Operand ca{ws + f.cut_a, a.N, (int64_t)a.E * kBk, ldz, 1}, cb{ws + f.cut_b, a.K, (int64_t)a.E * kBk, ldk, 1};
             if ((rc = make_map(&more.m[0], ca, 64, false)) || (rc = make_map(&more.m[1], cb, 64, true)))
                 return rc;
         }

@@ -2,6 +2,8 @@
 // weighted combine and its gradient.  Pair p = t*k + j of token t sits at grouped row pos[p]
 // (outside [0, rows): no row, e.g. a pair of another shard's expert).  Token-major throughout, so a
 // token's own row is read or written once and every grouped row once; no atomics.
+#include "kernels.cuh"
+#include "ptx.cuh"
 #include "routed.cuh"
 #include "vec.cuh"
 
@@ -9,26 +11,51 @@ namespace moe_mx {
 
 namespace {
 
-// One thread per (token, vector of V elements).
+constexpr int kMaxSlots = 32;
+constexpr int kAtOnce = 8; // slots whose rows are in flight together
+
+// Grouped rows of slots j0 .. j0 + 7 of token t; -1: none.
+__device__ __forceinline__ void slot_rows(const PermuteArgs &a, int t, int j0, int (&row)[kAtOnce])
+{
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+        row[j] = -1;
+        if (j0 + j < a.k) {
+            const int r = __ldg(a.pos + (size_t)t * a.k + j0 + j);
+            row[j] = r >= 0 && r < a.rows ? r : -1;
+        }
+    }
+}
+
+// One thread per (token, vector of V elements): x is read once, each grouped row written once, and
+// that traffic bounds it.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) dispatch_kernel(const PermuteArgs a)
 {
+    grid_dep_wait();
+    grid_dep_launch();
     const int t = blockIdx.x, c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
     if (c >= a.H)
         return;
     Raw<T, V> v;
     v.load(static_cast<const T *>(a.tok) + (size_t)t * a.H + c);
-    for (int j = 0; j < a.k; ++j) {
-        const int r = __ldg(a.pos + (size_t)t * a.k + j);
-        if (r >= 0 && r < a.rows)
-            *reinterpret_cast<Raw<T, V> *>(static_cast<T *>(a.grouped_out) + (size_t)r * a.H + c) = v;
+    for (int j0 = 0; j0 < a.k; j0 += kAtOnce) {
+        int row[kAtOnce];
+        slot_rows(a, t, j0, row);
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+            if (row[j] >= 0)
+                *reinterpret_cast<Raw<T, V> *>(static_cast<T *>(a.grouped_out) + (size_t)row[j] * a.H + c) = v;
     }
 }
 
-// out[t] = sum_j w[t,j] y[pos[t,j]], j ascending, in float32; one rounding at the end.
+// out[t] = sum_j w[t,j] y[pos[t,j]], j ascending, in float32; one rounding at the end.  One thread per
+// (token, vector), eight rows' loads in flight.
 template <typename T, typename TO, int V>
 __global__ void __launch_bounds__(256) combine_rows_kernel(const PermuteArgs a)
 {
+    grid_dep_wait();
+    grid_dep_launch();
     const int t = blockIdx.x, c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
     if (c >= a.H)
         return;
@@ -36,79 +63,102 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const PermuteArgs a)
 #pragma unroll
     for (int i = 0; i < V; ++i)
         acc[i] = 0.f;
-    for (int j = 0; j < a.k; ++j) {
-        const int r = __ldg(a.pos + (size_t)t * a.k + j);
-        if (r < 0 || r >= a.rows)
-            continue;
-        const float w = a.w ? __ldg(a.w + (size_t)t * a.k + j) : 1.f;
-        Raw<T, V> v;
-        float f[V];
-        v.load(static_cast<const T *>(a.grouped) + (size_t)r * a.H + c);
-        v.get(f);
+    for (int j0 = 0; j0 < a.k; j0 += kAtOnce) {
+        int row[kAtOnce];
+        Raw<T, V> v[kAtOnce];
+        slot_rows(a, t, j0, row);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            acc[i] = fmaf(w, f[i], acc[i]);
+        for (int j = 0; j < kAtOnce; ++j)
+            if (row[j] >= 0)
+                v[j].load(static_cast<const T *>(a.grouped) + (size_t)row[j] * a.H + c);
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+            if (row[j] >= 0) {
+                const float w = a.w ? __ldg(a.w + (size_t)t * a.k + j0 + j) : 1.f;
+                float f[V];
+                v[j].get(f);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    acc[i] = fmaf(w, f[i], acc[i]);
+            }
     }
     Raw<TO, V>::put(static_cast<TO *>(a.tok_out) + (size_t)t * a.H + c, acc);
 }
 
-constexpr int kMaxSlots = 32;
-
 // One CTA per token: dy[pos] = w dout (one rounding), dw = <dout, y[pos]> (float32, a fixed order),
 // and the gradient through w = softmax over the token's k chosen logits:
-// dlogits[id_j] += w_j (dw_j - sum_i w_i dw_i), every other logit 0.
+// dlogits[id_j] += w_j (dw_j - sum_i w_i dw_i), every other logit 0.  dout is read once for eight slots,
+// whose rows are in flight together and whose dot products meet in one reduction.
 template <typename T, typename TO, int V>
 __global__ void __launch_bounds__(256) combine_backward_kernel(const PermuteArgs a)
 {
-    __shared__ float s_part[8], s_dw[kMaxSlots], s_w[kMaxSlots];
+    grid_dep_wait();
+    grid_dep_launch();
+    __shared__ float s_part[8][kAtOnce], s_dw[kMaxSlots], s_w[kMaxSlots];
     __shared__ int s_id[kMaxSlots];
     const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const bool dots = a.dw || a.dlogits;
-    for (int j = 0; j < a.k; ++j) {
-        const size_t p = (size_t)t * a.k + j;
-        const int r = __ldg(a.pos + p);
-        const float w = __ldg(a.w + p);
-        float dot = 0.f;
-        if (r >= 0 && r < a.rows) {
-            for (int c = threadIdx.x * V; c < a.H; c += blockDim.x * V) {
-                Raw<TO, V> d;
-                float f[V], g[V];
-                d.load(static_cast<const TO *>(a.tok) + (size_t)t * a.H + c);
-                d.get(f);
-                if (dots) {
-                    Raw<T, V> y;
-                    y.load(static_cast<const T *>(a.grouped) + (size_t)r * a.H + c);
-                    y.get(g);
+    for (int j = threadIdx.x; j < a.k; j += blockDim.x) {
+        s_w[j] = __ldg(a.w + (size_t)t * a.k + j);
+        s_id[j] = a.dlogits ? __ldg(a.ids + (size_t)t * a.k + j) : -1;
+    }
+    __syncthreads();
+    for (int j0 = 0; j0 < a.k; j0 += kAtOnce) {
+        int row[kAtOnce];
+        slot_rows(a, t, j0, row);
+        float dot[kAtOnce] = {};
+        for (int c = threadIdx.x * V; c < a.H; c += blockDim.x * V) {
+            Raw<TO, V> d;
+            Raw<T, V> y[kAtOnce];
+            float f[V], g[V];
+            d.load(static_cast<const TO *>(a.tok) + (size_t)t * a.H + c);
+            if (dots) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        dot = fmaf(f[i], g[i], dot);
-                }
-                if (a.grouped_out) {
+                for (int j = 0; j < kAtOnce; ++j)
+                    if (row[j] >= 0)
+                        y[j].load(static_cast<const T *>(a.grouped) + (size_t)row[j] * a.H + c);
+            }
+            d.get(f);
+            if (a.grouped_out) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        g[i] = w * f[i];
-                    Raw<T, V>::put(static_cast<T *>(a.grouped_out) + (size_t)r * a.H + c, g);
-                }
+                for (int j = 0; j < kAtOnce; ++j)
+                    if (row[j] >= 0) {
+                        const float w = s_w[j0 + j];
+#pragma unroll
+                        for (int i = 0; i < V; ++i)
+                            g[i] = w * f[i];
+                        Raw<T, V>::put(static_cast<T *>(a.grouped_out) + (size_t)row[j] * a.H + c, g);
+                    }
+            }
+            if (dots) {
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j)
+                    if (row[j] >= 0) {
+                        y[j].get(g);
+#pragma unroll
+                        for (int i = 0; i < V; ++i)
+                            dot[j] = fmaf(f[i], g[i], dot[j]);
+                    }
             }
         }
         if (!dots)
             continue;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-        if (lane == 0)
-            s_part[warp] = dot;
+        for (int j = 0; j < kAtOnce; ++j) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], o);
+            if (lane == 0)
+                s_part[warp][j] = dot[j];
+        }
         __syncthreads();
-        if (threadIdx.x == 0) {
+        if (threadIdx.x < kAtOnce && j0 + threadIdx.x < a.k) {
             float d = 0.f;
             for (int i = 0; i < nw; ++i)
-                d += s_part[i];
-            s_dw[j] = d;
-            s_w[j] = w;
-            if (a.dlogits)
-                s_id[j] = __ldg(a.ids + p);
+                d += s_part[i][threadIdx.x];
+            s_dw[j0 + threadIdx.x] = d;
             if (a.dw)
-                a.dw[p] = d;
+                a.dw[(size_t)t * a.k + j0 + threadIdx.x] = d;
         }
         __syncthreads();
     }
@@ -146,19 +196,16 @@ template <typename F> void by_type(int type, F f)
 
 } // namespace
 
-// Rows are read and written in vectors of 8 elements when every row starts on 16 bytes.
+// Rows are read and written in vectors of 8 elements when every row starts on 16 bytes.  All are
+// programmatic dependents: each waits for what precedes it in the stream before its first access.
 void launch_dispatch(const PermuteArgs &a, cudaStream_t s)
 {
     by_type(a.type, [&](auto x) {
         using T = decltype(x);
         int threads;
-        if (a.H % 8 == 0) {
-            const dim3 g = row_grid(a.T, a.H / 8, &threads);
-            dispatch_kernel<T, 8><<<g, threads, 0, s>>>(a);
-        } else {
-            const dim3 g = row_grid(a.T, a.H, &threads);
-            dispatch_kernel<T, 1><<<g, threads, 0, s>>>(a);
-        }
+        const bool vec = a.H % 8 == 0;
+        const dim3 g = row_grid(a.T, vec ? a.H / 8 : a.H, &threads);
+        launch_kernel(vec ? dispatch_kernel<T, 8> : dispatch_kernel<T, 1>, g, dim3(threads), 0, s, true, a);
     });
 }
 
@@ -169,13 +216,10 @@ void launch_combine_rows(const PermuteArgs &a, cudaStream_t s)
             using T = decltype(x);
             using TO = decltype(y);
             int threads;
-            if (a.H % 8 == 0) {
-                const dim3 g = row_grid(a.T, a.H / 8, &threads);
-                combine_rows_kernel<T, TO, 8><<<g, threads, 0, s>>>(a);
-            } else {
-                const dim3 g = row_grid(a.T, a.H, &threads);
-                combine_rows_kernel<T, TO, 1><<<g, threads, 0, s>>>(a);
-            }
+            const bool vec = a.H % 8 == 0;
+            const dim3 g = row_grid(a.T, vec ? a.H / 8 : a.H, &threads);
+            launch_kernel(vec ? combine_rows_kernel<T, TO, 8> : combine_rows_kernel<T, TO, 1>, g, dim3(threads), 0, s,
+                          true, a);
         });
     });
 }
@@ -186,10 +230,11 @@ void launch_combine_backward(const PermuteArgs &a, cudaStream_t s)
         by_type(a.io_type, [&](auto y) {
             using T = decltype(x);
             using TO = decltype(y);
-            if (a.H % 8 == 0)
-                combine_backward_kernel<T, TO, 8><<<a.T, 256, 0, s>>>(a);
-            else
-                combine_backward_kernel<T, TO, 1><<<a.T, 256, 0, s>>>(a);
+            int threads; // equal rounds over the row
+            const bool vec = a.H % 8 == 0;
+            row_grid(a.T, vec ? a.H / 8 : a.H, &threads);
+            launch_kernel(vec ? combine_backward_kernel<T, TO, 8> : combine_backward_kernel<T, TO, 1>, dim3(a.T),
+                          dim3(threads), 0, s, true, a);
         });
     });
 }
