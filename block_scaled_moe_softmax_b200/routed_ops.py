@@ -83,7 +83,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def _empty(shape, dtype, like, stream):
     """A new tensor that the call's stream uses first (the allocator learns of a stream of its own)."""
-    t = like.new_empty(shape, dtype=dtype)
+    t = like.new_empty(*shape, dtype=dtype)
     if isinstance(stream, torch.cuda.Stream):
         t.record_stream(stream)
     return t
@@ -264,7 +264,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
         _tensor(preact, "preact", x, x.dtype, (rows, N))
     dt, ot = _type(x, "x"), _type(out, "out")
     need = _linear_workspace(E, rows, N, K, dt, act, ot)
-    ws = _empty(need, torch.uint8, x, stream) if need else None
+    ws = _empty((need,), torch.uint8, x, stream) if need else None
     _call("moe_mx_linear", x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), counts, pad, E, rows, N, K, dt, act,
           ot, out.data_ptr(), _ptr(preact), _ptr(ws), need, on)
     return out
@@ -290,7 +290,7 @@ def linear_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, preact
     dw = _out(dw, w.shape, x.dtype, x, "dw", stream) if weight_grad else None
     db = _empty((E, N) if E else (N,), torch.float32, x, stream) if bias_grad else None
     need = _linear_backward_workspace(E, rows, N, K, dt, act, gt)
-    ws = _empty(need, torch.uint8, x, stream) if need else None
+    ws = _empty((need,), torch.uint8, x, stream) if need else None
     _call("moe_mx_linear_backward", dout.data_ptr(), x.data_ptr(), w.data_ptr(), _ptr(preact), counts, pad, E, rows, N,
           K, dt, act, gt, _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), need, on)
     return dx, dw, db

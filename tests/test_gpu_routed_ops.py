@@ -1,5 +1,8 @@
 """The routed operators (dispatch, combine, linear and their gradients) against plain float64 code."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -184,16 +187,44 @@ def test_linear_dense(M, N, K, act, bias, residual, dtype, out):
     _check_linear(x, w, b, res, act, out)
 
 
+FEW = [  # up to 16 rows: one launch, k shared by warps and the CTAs of a cluster
+    (1, 384, 7168), (3, 40, 7168), (9, 34, 4104), (16, 10000, 1000), (8, 9480, 264), (5, 16, 8), (13, 130, 24),
+    (16, 4096, 2056),
+]
+
+
+@pytest.mark.parametrize("M,N,K", FEW)
+@pytest.mark.parametrize("act,bias,residual,dtype,out", [
+    ("none", True, True, BF, F), ("gelu", True, False, HF, HF), ("swiglu", True, True, BF, BF)])
+def test_linear_few_rows(M, N, K, act, bias, residual, dtype, out):
+    x, w, b, res, _ = _linear_inputs(M, N, K, dtype, out, act, bias, residual, 70)
+    _check_linear(x, w, b, res, act, out)
+
+
+@pytest.mark.parametrize("M,N,K,act", [(1000, 384, 7168, "none"), (300, 264, 3000, "none"), (520, 256, 2048, "swiglu"),
+                                       (40, 400, 7168, "silu"), (600, 34, 1040, "swiglu")])
+def test_linear_float32_outputs_keep_their_precision(M, N, K, act):
+    """float32 outputs of long products.  The sum is kept in chains of 512 of k, 32 tensor-core additions that
+    may truncate by 2^-23 of a running sum of norm sqrt(i / 32): 21.3 x 2^-23 = 2.5e-6 of a chain's norm at
+    most, the same of the whole (chains add up in quadrature), and 14 rounding additions."""
+    x, w, b, _, _ = _linear_inputs(M, N, K, BF, F, act, True, False, 71)
+    got = ops.linear(x, w, b, activation=act, out_dtype=F)
+    want, _, bound, _ = ref.linear64(x, w, b, None, act)
+    ref.close(got, want, bound, "out")
+    assert float((got.to(ref.F64) - want).norm() / want.norm()) <= 3e-6
+
+
 GROUPED = [  # T, E, k, N, K, drop, hot
     (1, 1, 1, 64, 64, 0.0, None), (5, 6, 2, 40, 24, 0.0, None), (200, 3, 1, 96, 80, 0.2, None),
     (300, 8, 2, 256, 136, 0.0, 2), (700, 5, 2, 130, 70, 0.0, 0), (64, 40, 8, 264, 128, 0.3, None),
-    (9, 6, 2, 66, 33, 1.0, None),
+    (9, 6, 2, 66, 33, 1.0, None), (900, 4, 2, 320, 1100, 0.0, 1), (130, 7, 1, 34, 600, 0.0, None),
 ]
 
 
 @pytest.mark.parametrize("T,E,k,N,K,drop,hot", GROUPED)
 @pytest.mark.parametrize("act,bias,residual,dtype,out", [
-    ("none", True, False, BF, BF), ("swiglu", True, False, BF, BF), ("gelu", False, True, HF, F)])
+    ("none", True, False, BF, BF), ("swiglu", True, False, BF, BF), ("gelu", False, True, HF, F),
+    ("swiglu", True, True, HF, F)])
 def test_linear_grouped(T, E, k, N, K, drop, hot, act, bias, residual, dtype, out):
     r = ref.make_routing(T, E, k, 12, drop, hot)
     x, w, b, res, _ = _linear_inputs(r.rows, N, K, dtype, out, act, bias, residual, 13, E)
@@ -439,6 +470,29 @@ def test_another_stream_is_used():
     out = ops.linear(x, w, stream=s)
     s.synchronize()
     ref.close(out, *[a for i, a in enumerate(ref.linear64(torch.ones_like(x), w, None, None, "none")) if i in (0, 2)], "out")
+
+
+def test_first_call_of_a_process_may_be_captured():
+    code = """
+import torch
+from block_scaled_moe_softmax_b200 import routed_ops as ops
+x = torch.ones(300, 128, dtype=torch.bfloat16, device='cuda')
+w = torch.ones(64, 128, dtype=torch.bfloat16, device='cuda')
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y = ops.linear(x, w)
+    dx, dw, db = ops.linear_backward(y, x, w, bias_grad=True)
+    z = ops.linear(x[:1], w, out_dtype=torch.float32)
+g.replay()
+torch.cuda.synchronize()
+assert (y == 128).all() and (dx == 128 * 64).all() and (dw == 300 * 128).all() and (db == 300 * 128).all()
+assert (z == 128).all()
+print('captured')
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_routing_of_the_library_feeds_the_operators():
