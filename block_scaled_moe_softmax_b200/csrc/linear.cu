@@ -424,7 +424,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 2)
         tmem_alloc_pair(tmem_slot, 512);
     grid_dep_wait(); // everything this kernel reads, and the buffers it writes
-    grid_dep_launch();
     if (C::kPrefix && warp == 3 && g.seg.E && !g.seg_k) {
         int run = 0;
         for (int e0 = 0; e0 < g.seg.E; e0 += 32) {
@@ -454,6 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncthreads();
     cluster_sync(); // barriers of both CTAs are set up
     tc_fence_after();
+    grid_dep_launch(); // this CTA holds its TMEM: a kernel launched early cannot take it first
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + C::kOffBar + 8 * C::kNumBar);
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     Tile t;
@@ -949,20 +949,75 @@ __global__ void __launch_bounds__(256) reduce_kernel(const float *__restrict__ p
 // ---------------------------------------------------------------- unaligned rows
 // TMA reads rows that start on 16 bytes: operands whose row length is not a multiple of 8 are first
 // copied to rows of the next multiple (the pad is not read: the tensor map ends at the true length).
-__global__ void __launch_bounds__(256) pack_kernel(const uint16_t *__restrict__ src, uint16_t *__restrict__ dst,
-                                                   int64_t rows, int cols, int ld)
+struct PackArgs {
+    const uint16_t *src[2]; // x, w; nullptr: no copy
+    uint16_t *dst[2];
+    int64_t rows[2];
+    int cols, ld;
+    Segments seg;           // of x's rows: padding is left out
+};
+
+// One CTA per row (grid y: x or w); a thread copies 8 elements, two at a time from aligned words that its
+// row may start in the middle of.
+__global__ void __launch_bounds__(256) pack_kernel(const PackArgs a)
 {
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int c = threadIdx.x; c < cols; c += blockDim.x)
-            dst[r * ld + c] = src[r * cols + c];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int o = a.src[0] ? blockIdx.y : 1;
+    for (int64_t r = blockIdx.x; r < a.rows[o]; r += gridDim.x) {
+        int e;
+        int64_t end;
+        if (o == 0 && a.seg.E && !find_segment(a.seg, r, e, end))
+            continue;
+        const uint16_t *src = a.src[o] + r * a.cols;
+        uint16_t *dst = a.dst[o] + r * a.ld;
+        const bool odd = reinterpret_cast<uintptr_t>(src) & 2;
+        for (int c = threadIdx.x * 8; c < a.cols; c += 256 * 8) {
+            if (c + 8 > a.cols) {
+                for (int i = c; i < a.cols; ++i)
+                    dst[i] = src[i];
+                continue;
+            }
+            uint32_t v[4];
+            if (odd) { // the words around the eight: the first holds the element before them, which is
+                       // in the buffer (an odd row is not the first), and the last ends with the eighth
+                const uint32_t *p = reinterpret_cast<const uint32_t *>(src + c - 1);
+                uint32_t lo = p[0];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t hi = i < 3 ? p[i + 1] : src[c + 7];
+                    v[i] = __funnelshift_r(lo, hi, 16);
+                    lo = hi;
+                }
+            } else {
+                const uint32_t *p = reinterpret_cast<const uint32_t *>(src + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = p[i];
+            }
+            *reinterpret_cast<uint4 *>(dst + c) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    }
 }
 
-void launch_pack(const void *src, void *dst, int64_t rows, int cols, cudaStream_t s)
+// x and w (either may be absent) with aligned rows; nothing to do when K is a multiple of 8.
+cudaError_t launch_pack(const void *&x, int64_t x_rows, const Segments &seg, char *x_ws, const void *&w, int64_t w_rows,
+                        char *w_ws, int K, cudaStream_t s)
 {
-    const int64_t want = rows < 65536 ? rows : 65536;
-    pack_kernel<<<(unsigned)(want > 0 ? want : 1), 256, 0, s>>>(static_cast<const uint16_t *>(src),
-                                                                 static_cast<uint16_t *>(dst), rows, cols,
-                                                                 (int)round_up(cols, 8));
+    if (K % 8 == 0 || (!x && !w))
+        return cudaSuccess;
+    PackArgs a{};
+    a.src[0] = static_cast<const uint16_t *>(x), a.src[1] = static_cast<const uint16_t *>(w);
+    a.dst[0] = reinterpret_cast<uint16_t *>(x_ws), a.dst[1] = reinterpret_cast<uint16_t *>(w_ws);
+    a.rows[0] = x_rows, a.rows[1] = w_rows;
+    a.cols = K, a.ld = (int)round_up(K, 8), a.seg = seg;
+    const int64_t most = !x ? w_rows : !w ? x_rows : x_rows > w_rows ? x_rows : w_rows;
+    const dim3 grid((unsigned)(most < 148 * 8 ? most : 148 * 8), x && w ? 2 : 1);
+    if (x)
+        x = x_ws;
+    if (w)
+        w = w_ws;
+    return launch_kernel(pack_kernel, grid, dim3(256), 0, s, true, a);
 }
 
 // ---------------------------------------------------------------- launch
@@ -1508,14 +1563,6 @@ BackwardPlan plan_backward(int E, int64_t M, int N, int K, int act, int type, in
     return f;
 }
 
-const void *packed(const void *p, int64_t rows, int cols, char *ws, int64_t at, cudaStream_t s)
-{
-    if (cols % 8 == 0)
-        return p;
-    launch_pack(p, ws + at, rows, cols, s);
-    return ws + at;
-}
-
 // The sum of a split product's planes, through the epilogue.
 int launch_reduce(const float *planes, int splits, int64_t M, const Epi &e, cudaStream_t s)
 {
@@ -1565,10 +1612,15 @@ int launch_linear(const LinearArgs &a, cudaStream_t s)
     const ForwardPlan f = plan_linear(a.E, a.M, a.N, a.K, a.act, a.out_type == kTypeF32);
     char *ws = static_cast<char *>(a.ws);
     const int ld = (int)round_up(a.K, 8), experts = a.E ? a.E : 1;
-    const Operand x{packed(a.x, a.M, a.K, ws, f.x, s), a.K, a.M, ld, 1};
-    const Operand w{packed(a.w, (int64_t)experts * a.N, a.K, ws, f.w, s), a.K, a.N, ld, experts};
+    const Segments seg{a.counts, a.pad_offsets, a.E, a.M};
+    const void *xk = a.x, *wk = a.w;
+    const cudaError_t ce = launch_pack(xk, a.M, seg, ws + f.x, wk, (int64_t)experts * a.N, ws + f.w, a.K, s);
+    if (ce != cudaSuccess)
+        return cuda_fail(ce, "operand copy launch");
+    const Operand x{xk, a.K, a.M, ld, 1};
+    const Operand w{wk, a.K, a.N, ld, experts};
     Gemm g{};
-    g.seg = Segments{a.counts, a.pad_offsets, a.E, a.M};
+    g.seg = seg;
     g.M = (int)a.M, g.n_cols = a.No(), g.N = a.N, g.K = a.K;
     g.gated = a.act == kActSwiglu, g.act = a.act, g.fmt = a.type == kTypeBf16;
     g.bias = a.bias, g.residual = a.residual, g.out = a.out, g.preact = a.preact;
@@ -1624,7 +1676,11 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
     }
     const void *dz = f.direct ? a.dout : d.dz;
     const int ldz = f.direct ? a.N : d.ldz, ldk = (int)round_up(a.K, 8), experts = a.E ? a.E : 1;
-    const void *xk = a.dw && a.M > 0 ? packed(a.x, a.M, a.K, ws, f.x, s) : nullptr; // x with aligned rows
+    // x and w with aligned rows, where a product reads them
+    const void *xk = a.dw && a.M > 0 ? a.x : nullptr, *wk = a.dx && a.M > 0 ? a.w : nullptr;
+    cudaError_t pe = launch_pack(xk, a.M, seg, ws + f.x, wk, (int64_t)experts * a.N, ws + f.w, a.K, s);
+    if (pe != cudaSuccess)
+        return cuda_fail(pe, "operand copy launch");
     const bool cut = a.dw && a.E && a.M > 0;
     if (a.dbias || cut) {
         AfterArgs p{};
@@ -1643,7 +1699,7 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
     int rc;
     if (a.dx && a.M > 0) {
         const Operand oa{dz, a.N, a.M, ldz, 1};
-        const Operand ob{packed(a.w, (int64_t)experts * a.N, a.K, ws, f.w, s), a.K, a.N, ldk, experts};
+        const Operand ob{wk, a.K, a.N, ldk, experts};
         Gemm g{};
         g.seg = seg, g.M = (int)a.M, g.n_cols = g.N = a.K, g.K = a.N;
         g.fmt = a.type == kTypeBf16, g.out = a.dx, g.type = g.out_type = a.type, g.vec = a.K % 8 == 0;

@@ -13,8 +13,9 @@ gradients (the ``moe_mx_*`` entry points of the same names in include/moe_mx.h).
     dx = dispatch_backward(dg, r)
 
 Gradients are explicit calls, as everything in the library is.  Tensors are contiguous CUDA tensors of
-one device; a call is enqueued on ``stream`` (default: the tensors' device's current stream) and
-allocates only what it returns and its workspace, from torch's allocator.  Wrong types, shapes or
+one device; a call is enqueued on ``stream`` (a torch.cuda.Stream or a raw handle; default: the current
+stream of the tensors' device) and allocates only what it returns and its workspace, from torch's
+allocator, as under ``with torch.cuda.stream(stream)``.  Wrong types, shapes or
 devices raise TypeError or ValueError before anything is enqueued.  Output buffers may be passed in
 (``out``, ``dy``, ``dx``); rows of grouped buffers that hold no pair (padding) are never written.
 """
@@ -82,11 +83,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 
 def _empty(shape, dtype, like, stream):
-    """A new tensor that the call's stream uses first (the allocator learns of a stream of its own)."""
-    t = like.new_empty(*shape, dtype=dtype)
-    if isinstance(stream, torch.cuda.Stream):
-        t.record_stream(stream)
-    return t
+    """A new tensor of the call's stream: on another stream than the current one it comes from that
+    stream's pool, since memory freed on the current stream may still be in use there."""
+    if stream is None:
+        return like.new_empty(*shape, dtype=dtype)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=like.device)
+    with torch.cuda.stream(stream):
+        return like.new_empty(*shape, dtype=dtype)
 
 
 def _pairs(r: Routing, like):

@@ -472,6 +472,23 @@ def test_another_stream_is_used():
     ref.close(out, *[a for i, a in enumerate(ref.linear64(torch.ones_like(x), w, None, None, "none")) if i in (0, 2)], "out")
 
 
+def test_new_tensors_belong_to_the_calls_stream():
+    """Memory freed on the current stream while its kernels still run is not handed to a call on another
+    stream: the old tensor's late write would land in the call's result."""
+    s = torch.cuda.Stream()
+    x, w = rnd((256, 512), BF, 72), rnd((512, 512), BF, 73)
+    want = ops.linear(x, w)
+    torch.cuda.synchronize()
+    for handle in (s, s.cuda_stream):
+        old = torch.empty_like(want)
+        torch.cuda._sleep(20_000_000)
+        old.fill_(7.0)
+        del old  # freed on the current stream, its fill still to come
+        got = ops.linear(x, w, stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
 def test_first_call_of_a_process_may_be_captured():
     code = """
 import torch
