@@ -98,8 +98,10 @@ template <typename F> void by_half(int type, F f)
 // ---------------------------------------------------------------- matrix product
 // D[m, n] = sum_k A[m, k] B[n, k] on tcgen05, two CTAs to a 256 x BN tile (cta_group::2): each holds
 // 128 rows of A and half of B's rows in shared memory and 128 rows of the accumulator in its TMEM.
-// Warp 0 copies 64-deep k blocks in with TMA, warp 1 of the leader issues the MMAs, warps 4..11 take
-// a finished accumulator out while the next tile's runs in the other half of TMEM.
+// Warp 0 (and warp 2) copies 64-deep k blocks of A and B in with TMA, warp 1 of the leader issues the MMAs,
+// warps 4..11 take a finished accumulator out while the next tile's runs in the other half of TMEM,
+// and warp 3 finds the tiles ahead of them all (kAhead).  (One warp that found its tiles and issued four copies a
+// k block took 0.3 us a block and 1.1 us a tile: longer than the MMAs of a short product.)
 //
 // Operands with k contiguous (x and w of the forward pass, dz in dx) are K-major tiles; those with
 // k along the rows (w in dx; dz and x in dw) are read as they lie, as M- or N-major tiles.
@@ -123,11 +125,13 @@ struct Gemm {
     void *out, *preact;
     int act, N;           // columns of preact, and of each expert's bias
     int type, out_type, vec;
+    int wide_a, wide_b;   // an M- or N-major operand of whole 64-element groups: one copy takes all of them
     int64_t d_expert;     // elements from one expert's D to the next's (seg_k)
 };
 
 constexpr int kTileM = 256, kBk = 64, kMaxSeg = kMaxExperts;
 constexpr int kThreads = 384, kEpiWarps = 8;
+constexpr int kRing = 4, kTileInts = 12; // tiles decoded ahead, and the words of one
 constexpr unsigned long long kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
 
 template <int BN, bool kSwap> struct Cfg {
@@ -136,9 +140,11 @@ template <int BN, bool kSwap> struct Cfg {
     static constexpr bool kPrefix = kSwap || BN == 128;
     static constexpr int kStages = BN == 256 ? (kPrefix ? 5 : 6) : BN == 192 ? 6 : 7;
     static constexpr int kOffEpi = kStages * kStage, kOffBar = kOffEpi + kEpiWarps * 4096;
-    // barriers: full, empty per stage, 2 acc_full, 2 acc_empty, mma_done; then the TMEM address
-    static constexpr int kNumBar = 2 * kStages + 5;
-    static constexpr int kOffPrefix = kOffBar + kNumBar * 8 + 8;
+    // barriers: full, empty per stage, 2 acc_full, 2 acc_empty, mma_done, and full, empty of the tile ring;
+    // then the TMEM address, the ring, and the experts' tile counts
+    static constexpr int kNumBar = 2 * kStages + 5 + 2 * kRing;
+    static constexpr int kOffRing = (kOffBar + kNumBar * 8 + 8 + 15) / 16 * 16;
+    static constexpr int kOffPrefix = kOffRing + kRing * kTileInts * 4;
     static constexpr int kSmem = kOffPrefix + (kPrefix ? (kMaxSeg + 1) * 4 : 0) + 1024; // + alignment of the base
     static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
@@ -393,6 +399,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     using C = Cfg<BN, kSwap>;
     constexpr bool kPlain = kSwap ? kAMn : kBMn;  // a gradient: no bias, preact, activation or residual
     constexpr int kMostTok = kSum ? 128 : 256;    // kSwap: tokens of a tile (kSum keeps them in registers)
+    // M- or N-major operands may take two copies each: warp 2 issues B's (one warp for both is 2 % faster where
+    // each is one copy)
+    constexpr bool kSplit = kAMn || kBMn;
+    // Tiles are found ahead by warp 3; dense products with k contiguous, whose tiles take no search, let each
+    // warp find its own.  Measured: 8192 x 7168 x 2048 130 us so, 140 with warp 3; experts' products
+    // (search, short k) 1 to 5 % faster with warp 3.
+    constexpr bool kAhead = kSwap || kSplit || BN == 128;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *const sm = smem_raw + (base - smem_u32(smem_raw));
@@ -405,6 +418,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto acc_full = [&](int b) { return bar0 + 8u * (2 * S + b); };
     auto acc_empty = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
     const uint32_t mma_done = bar0 + 8u * (2 * S + 4), tmem_slot = bar0 + 8u * C::kNumBar;
+    auto tile_full = [&](uint32_t r) { return bar0 + 8u * (2 * S + 5 + r); };
+    auto tile_empty = [&](uint32_t r) { return bar0 + 8u * (2 * S + 5 + kRing + r); };
+    int4 *const ring = reinterpret_cast<int4 *>(sm + C::kOffRing);
     int32_t *const prefix = reinterpret_cast<int32_t *>(sm + C::kOffPrefix); // kPrefix only
 
     if (threadIdx.x == 0) {
@@ -417,6 +433,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(acc_empty(b), 2 * kEpiWarps);
         }
         mbar_init(mma_done, 1);
+        for (int r = 0; r < kRing; ++r) {
+            mbar_init(tile_full(r), 1);
+            mbar_init(tile_empty(r), kEpiWarps + (rank == 0 ? 2 : 1) + (kSplit ? 1 : 0)); // the warps that read tiles
+        }
         fence_mbar_init();
         prefetch_tensormap(&map_a);
         prefetch_tensormap(&map_b);
@@ -424,31 +444,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 2)
         tmem_alloc_pair(tmem_slot, 512);
     grid_dep_wait(); // everything this kernel reads, and the buffers it writes
-    if (C::kPrefix && warp == 3 && g.seg.E && !g.seg_k) {
-        int run = 0;
-        for (int e0 = 0; e0 < g.seg.E; e0 += 32) {
-            const int e = e0 + lane;
-            int n = 0;
-            if (e < g.seg.E) {
-                int first;
-                const int rows = segment_rows(g.seg, e, first);
-                int tok;
-                n = (kSwap ? token_tiles(rows, kMostTok, tok) : (rows + kTileM - 1) / kTileM) * g.nt;
-            }
-            int incl = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                if (lane >= o)
-                    incl += y;
-            }
-            if (e < g.seg.E)
-                prefix[e] = run + incl - n;
-            run += __shfl_sync(0xFFFFFFFFu, incl, 31);
-        }
-        if (lane == 0)
-            prefix[g.seg.E] = run;
-    }
     tc_fence_before();
     __syncthreads();
     cluster_sync(); // barriers of both CTAs are set up
@@ -457,19 +452,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + C::kOffBar + 8 * C::kNumBar);
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     Tile t;
+    // The c-th tile of this pair (whole warp); false after the last, or if a wait gave up.
+    auto next = [&](uint32_t &c) {
+        if (!kAhead)
+            return get_tile<BN, kSwap, kMostTok>(g, prefix, pair + (int)c++ * pairs, t);
+        const uint32_t r = c % kRing;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(tile_full(r), (c / kRing) & 1, &g_linear_err, kWaitNs)))
+            return false;
+        const int4 x = ring[r * 3], y = ring[r * 3 + 1], z = ring[r * 3 + 2];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(tile_empty(r));
+        ++c;
+        t.e = x.x, t.row = x.y, t.row_end = x.z, t.n0 = x.w;
+        t.k0 = y.x, t.nkb = y.y, t.rem = y.z, t.split = y.w;
+        t.tok = z.x;
+        return t.nkb >= 0;
+    };
+    uint32_t c = 0;
+    bool ok = true;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ copies
+    if (warp == 0 || (kSplit && warp == 2)) {
+        // ------------------------------------------------------------ copies: A, and B
         uint32_t it = 0; // k blocks issued
-        bool ok = true;
-        for (int i = pair; ok && get_tile<BN, kSwap, kMostTok>(g, prefix, i, t); i += pairs) {
+        while (ok && next(c)) {
             const int a_row = t.row + (int)rank * 128; // kSwap: weight rows (columns of D) from n0
             const int w_row = t.n0 + (int)rank * (g.gated ? 64 : 128), tok0 = t.row + (int)rank * (t.tok / 2);
             // kSwap: one box of 16, 32, 64 or 128 token rows, the least that holds the tile's half (a copy
             // of exactly its rows, 16 at a time, costs more in copies issued than it saves in bytes:
             // 0.54 against 0.37 us a k block at 224 tokens)
             const int box_log = t.tok > 128 ? 3 : t.tok > 64 ? 2 : t.tok > 32 ? 1 : 0;
-            const uint32_t bytes = kSwap ? C::kABytes + (2048u << box_log) : C::kStage;
+            const uint32_t bytes = C::kABytes + (kSwap ? 2048u << box_log : C::kBBytes);
             const int b_row = g.gated ? (int)rank * g.n_cols + t.n0 : t.n0 + (int)rank * (BN / 2);
             for (int kb = 0; kb < t.nkb; ++kb, ++it) {
                 const int s = it % S;
@@ -480,31 +493,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) {
                     const int k = t.k0 + kb * kBk;
                     const uint32_t bar = map_rank(full(s), 0);
-                    mbar_arrive_expect_tx_relaxed(bar, bytes);
+                    // one arrival for both operands; B's bytes may land before it, which the barrier counts
+                    if (warp == 0)
+                        mbar_arrive_expect_tx_relaxed(bar, bytes);
                     // the last block of a segment whose rows end inside it: its copy filled up with zeros
                     const bool cut = kAMn && kBMn && t.rem && kb == t.nkb - 1;
                     const int kr = cut ? t.e * kBk : k;
                     const uint32_t sa = base + s * C::kStage, sb = sa + C::kABytes;
-                    if (kSwap) {
+                    if (!kSplit || warp == 0) {
                         if (kAMn) {
-                            for (int j = 0; j < 2; ++j)
-                                tma_pair_3d(sa + j * 8192, &map_a, w_row + j * 64, k, t.e, bar);
-                        } else if (g.gated) {
+                            const CUtensorMap *m = !kSwap && cut ? &map_c.m[0] : &map_a;
+                            const int row = kSwap ? w_row : a_row, e = kSwap ? t.e : 0;
+                            if (g.wide_a)
+                                tma_pair_4d(sa, m, 0, kr, row / 64, e, bar);
+                            else
+                                for (int j = 0; j < 2; ++j)
+                                    tma_pair_3d(sa + j * 8192, m, row + j * 64, kr, e, bar);
+                        } else if (kSwap && g.gated) {
                             tma_pair_5d(sa, &map_a, k, 0, 0, w_row / 16, t.e, bar);
-                        } else {
+                        } else if (kSwap) {
                             tma_pair_3d(sa, &map_a, k, w_row, t.e, bar);
+                        } else {
+                            tma_pair_2d(sa, &map_a, k, a_row, bar);
                         }
-                        tma_pair_2d(sb, box_log == 3 ? &map_b : &map_c.m[box_log], k, tok0, bar);
-                    } else if (kAMn) {
-                        for (int j = 0; j < 2; ++j)
-                            tma_pair_2d(sa + j * 8192, cut ? &map_c.m[0] : &map_a, a_row + j * 64, kr, bar);
-                    } else {
-                        tma_pair_2d(sa, &map_a, k, a_row, bar);
                     }
-                    if (kSwap) {
+                    if (kSplit && warp == 0) {
+                    } else if (kSwap) {
+                        tma_pair_2d(sb, box_log == 3 ? &map_b : &map_c.m[box_log], k, tok0, bar);
                     } else if (kBMn) {
-                        for (int j = 0; j < BN / 128; ++j)
-                            tma_pair_3d(sb + j * 8192, cut ? &map_c.m[1] : &map_b, b_row + j * 64, kr, g.seg_k ? 0 : t.e, bar);
+                        const CUtensorMap *m = cut ? &map_c.m[1] : &map_b;
+                        const int e = g.seg_k ? 0 : t.e;
+                        if (g.wide_b)
+                            tma_pair_4d(sb, m, 0, kr, b_row / 64, e, bar);
+                        else
+                            for (int j = 0; j < BN / 128; ++j)
+                                tma_pair_3d(sb + j * 8192, m, b_row + j * 64, kr, e, bar);
                     } else {
                         tma_pair_3d(sb, &map_b, k, b_row, t.e, bar);
                     }
@@ -514,20 +537,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // Before either CTA may exit, every copy has landed (all report to the leader's barriers; a wait
         // that gave up leaves some unread) and every commit has reached this CTA's barriers.
-        for (int j = 0; j < S; ++j)
-            if (it > (uint32_t)j) {
-                const uint32_t last = it - 1 - j;
-                if (rank == 0)
-                    mbar_wait_bounded(full(last % S), (last / S) & 1, nullptr, kDrainNs);
-                mbar_wait_bounded(empty(last % S), (last / S) & 1, nullptr, kDrainNs);
+        if (warp == 0) {
+            for (int j = 0; j < S; ++j)
+                if (it > (uint32_t)j) {
+                    const uint32_t last = it - 1 - j;
+                    if (rank == 0)
+                        mbar_wait_bounded(full(last % S), (last / S) & 1, nullptr, kDrainNs);
+                    mbar_wait_bounded(empty(last % S), (last / S) & 1, nullptr, kDrainNs);
+                }
+            if (rank == 1)
+                mbar_wait_bounded(mma_done, 0, nullptr, kDrainNs); // the leader's last commit
+        }
+    } else if (kAhead && warp == 3) {
+        // ------------------------------------------------------------ tiles
+        if (C::kPrefix && g.seg.E && !g.seg_k) {
+            int run = 0;
+            for (int e0 = 0; e0 < g.seg.E; e0 += 32) {
+                const int e = e0 + lane;
+                int n = 0;
+                if (e < g.seg.E) {
+                    int first;
+                    const int rows = segment_rows(g.seg, e, first);
+                    int tok;
+                    n = (kSwap ? token_tiles(rows, kMostTok, tok) : (rows + kTileM - 1) / kTileM) * g.nt;
+                }
+                int incl = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                    if (lane >= o)
+                        incl += y;
+                }
+                if (e < g.seg.E)
+                    prefix[e] = run + incl - n;
+                run += __shfl_sync(0xFFFFFFFFu, incl, 31);
             }
-    } else if (warp == 1 && rank == 1) {
-        mbar_wait_bounded(mma_done, 0, nullptr, kDrainNs); // the leader's last commit
-    } else if (warp == 1) {
+            if (lane == 0)
+                prefix[g.seg.E] = run;
+            __syncwarp();
+        }
+        bool more = true;
+        for (int i = pair; more; i += pairs, ++c) {
+            more = get_tile<BN, kSwap, kMostTok>(g, prefix, i, t);
+            const uint32_t r = c % kRing;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(tile_empty(r), ((c / kRing) & 1) ^ 1, &g_linear_err, kWaitNs)))
+                break;
+            if (lane == 0) {
+                ring[r * 3] = make_int4(t.e, t.row, t.row_end, t.n0);
+                ring[r * 3 + 1] = make_int4(t.k0, more ? t.nkb : -1, t.rem, t.split);
+                ring[r * 3 + 2] = make_int4(t.tok, 0, 0, 0);
+                mbar_arrive(tile_full(r));
+            }
+            __syncwarp();
+        }
+    } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------------ MMAs
         uint32_t it = 0, n = 0;
-        bool ok = true;
-        for (int i = pair; ok && get_tile<BN, kSwap, kMostTok>(g, prefix, i, t); i += pairs) {
+        while (ok && next(c)) {
             const uint32_t idesc = idesc_f16(g.fmt, kAMn, kBMn, kTileM, kSwap ? t.tok : BN);
             for (int kb = 0; ok && kb < t.nkb;) {
                 const int buf = n & 1;
@@ -574,7 +640,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int cols = g.gated ? BN / 4 : BN / 2; // columns of D this warp takes
         const int rl = lane >> 2, c8 = (lane & 3) * 8;
         uint32_t n = 0;
-        bool ok = true;
         // 32 columns of this warp's 32 rows (lane: row) through shared memory: lane l then holds row
         // 8 j + l / 4, columns 8 (l % 4) .. + 7
         auto turn = [&](const uint32_t (&r)[32], float (&v)[4][8]) {
@@ -607,7 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mbar_arrive_relaxed(map_rank(acc_empty(n & 1), 0)); // its TMEM reads are done (wait::ld)
             ++n;
         };
-        for (int i = pair; ok && get_tile<BN, kSwap, kMostTok>(g, prefix, i, t); i += pairs) {
+        while (ok && next(c)) {
             // gradients have no bias, preact, activation or residual
             const Epi ep = kPlain ? Epi{nullptr, nullptr, g.out, nullptr, kActNone, g.N, g.n_cols, g.type, g.out_type, g.vec}
                                 : Epi{g.bias ? g.bias + (size_t)t.e * g.N : nullptr, g.residual, g.out, g.preact, g.act,
@@ -1274,12 +1339,26 @@ struct Operand {
     int experts; // planes of rows (B of a rows-segmented product), else 1
 };
 
+// rank 2 (x of kSwap, one plane) or 3; box of 64 elements x box_rows rows.
 int make_map(CUtensorMap *map, const Operand &o, int box_rows, bool three)
 {
     const cuuint64_t dims[3] = {(cuuint64_t)o.inner, (cuuint64_t)o.rows, (cuuint64_t)o.experts};
     const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, (cuuint64_t)o.ld * 2 * o.rows};
     const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
     return encode_nd(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, three ? 3 : 2, o.p, dims, strides, box);
+}
+
+// An operand whose contiguous dimension is M or N, in boxes of 64 rows of k x `groups` groups of 64 elements
+// when its rows are whole groups (wide), else of one group (a group may not run over the last row's end).
+int make_map_mn(CUtensorMap *map, const Operand &o, int groups, int *wide)
+{
+    *wide = o.inner % 64 == 0;
+    if (!*wide)
+        return make_map(map, o, 64, true);
+    const cuuint64_t dims[4] = {64, (cuuint64_t)o.rows, (cuuint64_t)o.inner / 64, (cuuint64_t)o.experts};
+    const cuuint64_t strides[3] = {(cuuint64_t)o.ld * 2, 128, (cuuint64_t)o.ld * 2 * o.rows};
+    const cuuint32_t box[4] = {64, 64, (cuuint32_t)groups, 1};
+    return encode_nd(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, o.p, dims, strides, box);
 }
 
 // tiles: an upper bound of the product's tiles (the kernel finds a grouped product's on the device)
@@ -1291,7 +1370,8 @@ int run_gemm(Gemm &g, int bn, bool sum, const Operand &a, const Operand &b, int6
         return fail(MOE_MX_ERR_UNSUPPORTED, "the product has %lld tiles", (long long)tiles);
     CUtensorMap ma, mb;
     int rc;
-    if ((rc = make_map(&ma, a, kAMn ? 64 : 128, false)) || (rc = make_map(&mb, b, kBMn ? 64 : bn / 2, true)))
+    if ((rc = kAMn ? make_map_mn(&ma, a, 2, &g.wide_a) : make_map(&ma, a, 128, false)) ||
+        (rc = kBMn ? make_map_mn(&mb, b, bn / 128, &g.wide_b) : make_map(&mb, b, bn / 2, true)))
         return rc;
     if constexpr (!kBMn)
         if (sum)
@@ -1322,7 +1402,7 @@ int run_swap(Gemm &g, bool sum, const Operand &x, const Operand &w, int64_t tile
         const cuuint32_t box[5] = {64, 16, 2, 4, 1};
         rc = encode_nd(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, w.p, dims, strides, box);
     } else {
-        rc = make_map(&ma, w, kWMn ? 64 : 128, true);
+        rc = kWMn ? make_map_mn(&ma, w, 2, &g.wide_a) : make_map(&ma, w, 128, true);
     }
     // the boxes that the tiles may use: a dense product's are tiles of g.tok tokens, and a shorter last one
     const int most = g.seg.E ? 256 : g.tok;
@@ -1742,7 +1822,8 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
         MoreMaps more{};
         if (a.E) {
             const Operand ca{ws + f.cut_a, a.N, (int64_t)a.E * kBk, ldz, 1}, cb{ws + f.cut_b, a.K, (int64_t)a.E * kBk, ldk, 1};
-            if ((rc = make_map(&more.m[0], ca, 64, false)) || (rc = make_map(&more.m[1], cb, 64, true)))
+            int wide; // as of the operands themselves
+            if ((rc = make_map_mn(&more.m[0], ca, 2, &wide)) || (rc = make_map_mn(&more.m[1], cb, f.dw.bn / 128, &wide)))
                 return rc;
         }
         if ((rc = run_gemm<true, true>(g, f.dw.bn, false, oa, ob, (int64_t)g.mt * g.nt * (a.E ? a.E : g.splits), s, more)))

@@ -79,6 +79,16 @@ __device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+__device__ __forceinline__ void tma_pair_4d(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z,
+                                            int32_t u, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ void tma_pair_5d(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z,
                                             int32_t u, int32_t v, uint32_t bar)
 {
