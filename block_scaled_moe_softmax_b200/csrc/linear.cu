@@ -58,10 +58,10 @@ struct Segments {
 // Valid rows of expert e's segment, and its first row (none of a segment that starts outside the buffer).
 __device__ __forceinline__ int segment_rows(const Segments &s, int e, int &first)
 {
-    first = __ldg(s.pad_offsets + e);
+    first = s.pad_offsets[e];
     if (first < 0 || first >= s.M)
         return 0;
-    return max(0, min(__ldg(s.counts + e), (int)(s.M - first)));
+    return max(0, min(s.counts[e], (int)(s.M - first)));
 }
 
 // The segment holding row `r0` (a multiple of 64): its expert, and the end of its valid rows.
@@ -75,7 +75,7 @@ __device__ __forceinline__ bool find_segment(const Segments &s, int64_t r0, int 
     int lo = 0, hi = s.E; // the last e with pad_offsets[e] <= r0
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (__ldg(s.pad_offsets + mid) <= r0)
+        if (s.pad_offsets[mid] <= r0)
             lo = mid;
         else
             hi = mid;
@@ -320,7 +320,7 @@ template <int R> __device__ __forceinline__ void add_bias(const float *b, const 
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float f = w.n + i < g.n_cols ? __ldg(b + w.n + i) : 0.f;
+        const float f = w.n + i < g.n_cols ? b[w.n + i] : 0.f;
 #pragma unroll
         for (int j = 0; j < R; ++j)
             v[j][i] += f;
@@ -965,7 +965,7 @@ __device__ __forceinline__ void load_f32x8(const float *p, float (&f)[8])
 }
 
 // out = epilogue(sum over the splits' float32 planes, in order); one thread per 8 columns of a row.
-__global__ void __launch_bounds__(256) reduce_kernel(const float *__restrict__ planes, int splits, int M, Epi g)
+__global__ void __launch_bounds__(256) reduce_kernel(const float *planes, int splits, int M, Epi g)
 {
     grid_dep_wait();
     grid_dep_launch();
@@ -1136,7 +1136,7 @@ Plan plan_dense(int64_t M, int cols, int kb, bool gated, bool mn, bool f32, bool
 // memory rate, or launch latency.  Weight rows are the A operand of 16 x 8 x 16 warp MMAs, tokens the
 // B operand; a warp takes kR x 16 weight rows over a slice of k, the 8 warps of a CTA and the CTAs of a
 // cluster share k, and the partial sums meet in shared memory (a fixed order, one launch, where
-// a split tile product writes planes and launches a second kernel: 16.7 -> 10 us a call of
+// a split tile product writes planes and launches a second kernel: 16.7 -> 8.6 us a call of
 // 384 x 7168, most of it the host's).  Within a 32-element k block lane t of a row's four holds elements
 // 8t .. 8t + 7 of both operands (one 16-byte load), which the two MMAs take in the same order.
 constexpr int kSmallRows = 16, kSmallWarps = 8, kMaxCluster = 8;
@@ -1201,10 +1201,10 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(const SmallArgs
             const bool in = ku + 8 * t < k1; // K is a multiple of 8: 8 elements are in or out together
 #pragma unroll
             for (int r = 0; r < 2 * kR; ++r)
-                wv[u][r] = in && wok[r] ? __ldcs(reinterpret_cast<const uint4 *>(wp[r] + ku)) : make_uint4(0, 0, 0, 0);
+                wv[u][r] = in && wok[r] ? load_once(wp[r] + ku) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int b = 0; b < kNb; ++b)
-                xv[u][b] = in && xok[b] ? __ldg(reinterpret_cast<const uint4 *>(xp[b] + ku)) : make_uint4(0, 0, 0, 0);
+                xv[u][b] = in && xok[b] ? *reinterpret_cast<const uint4 *>(xp[b] + ku) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u)
@@ -1251,9 +1251,9 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(const SmallArgs
                     up += load_rank(&total[(16 + c) * (kNb * 8) + m], q);
             }
             if (e.bias) {
-                z += __ldg(e.bias + n);
+                z += e.bias[n];
                 if (kGated)
-                    up += __ldg(e.bias + cols + n);
+                    up += e.bias[cols + n];
             }
             if (e.preact) {
                 T *p = static_cast<T *>(e.preact) + (size_t)m * e.N + n;
@@ -1288,9 +1288,9 @@ int launch_small(const SmallArgs &args, int type, cudaStream_t s)
     // 32 weight rows a CTA halve the reads of x; 16 where that leaves SMs without a CTA
     const bool two = gated || a.N >= 32 * 296;
     const int tiles = (a.epi.n_cols + (two && !gated ? 31 : 15)) / (two && !gated ? 32 : 16);
-    // k is shared by as many CTAs of a cluster as two CTAs to each SM take, each warp keeping 64 elements
+    // k is shared by the CTAs of a cluster until there are two to four CTAs an SM, each warp keeping 64 elements
     int ranks = 1;
-    while (ranks < kMaxCluster && tiles * ranks * 2 <= 2 * 2 * kPairs * 2 && a.K >= 64 * kSmallWarps * ranks * 2)
+    while (ranks < kMaxCluster && tiles * ranks <= 4 * kPairs && a.K >= 64 * kSmallWarps * ranks * 2)
         ranks *= 2;
     a.k_warp = (int)round_up((a.K + kSmallWarps * ranks - 1) / (kSmallWarps * ranks), 32);
     cudaLaunchConfig_t cfg = {};

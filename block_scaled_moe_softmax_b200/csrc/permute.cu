@@ -24,7 +24,7 @@ template <int n> __device__ __forceinline__ void slot_rows(const PermuteArgs &a,
     for (int j = 0; j < n; ++j) {
         row[j] = -1;
         if (j0 + j < a.k) {
-            const int r = __ldg(a.pos + (size_t)t * a.k + j0 + j);
+            const int r = a.pos[(size_t)t * a.k + j0 + j];
             row[j] = r >= 0 && r < a.rows ? r : -1;
         }
     }
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const PermuteArgs a)
 #pragma unroll
         for (int j = 0; j < kCombineRows; ++j)
             if (row[j] >= 0) {
-                const float w = a.w ? __ldg(a.w + (size_t)t * a.k + j0 + j) : 1.f;
+                const float w = a.w ? a.w[(size_t)t * a.k + j0 + j] : 1.f;
                 float f[V];
                 v[j].get(f);
 #pragma unroll
@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const PermuteArgs
     const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const bool dots = a.dw || a.dlogits;
     for (int j = threadIdx.x; j < a.k; j += blockDim.x) {
-        s_w[j] = __ldg(a.w + (size_t)t * a.k + j);
-        s_id[j] = a.dlogits ? __ldg(a.ids + (size_t)t * a.k + j) : -1;
+        s_w[j] = a.w[(size_t)t * a.k + j];
+        s_id[j] = a.dlogits ? a.ids[(size_t)t * a.k + j] : -1;
     }
     __syncthreads();
     for (int j0 = 0; j0 < a.k; j0 += kBackwardRows) {

@@ -38,6 +38,19 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __half)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// 16 bytes that are read once.  Volatile, as plain loads are used throughout and not __ldg or restrict
+// pointers: a load that the compiler takes for one of constant data may move above the wait for
+// the kernel that writes it.
+__device__ __forceinline__ uint4 load_once(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // V raw elements in flight, converted when they are used.
 template <typename T, int V> struct Raw;
 template <typename T> struct Raw<T, 1> {

@@ -489,6 +489,111 @@ def test_new_tensors_belong_to_the_calls_stream():
         assert torch.equal(got, want)
 
 
+def test_streams_forked_inside_a_capture():
+    p, _ = _stage_inputs(T=270)
+    w = rnd((192, 192), BF, 74)
+    want = [ops.linear(p["x"], w, activation="silu"), ops.linear(p["dout"], w, activation="gelu")]
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        x = p["x"] + 0  # a kernel of another library right before and after
+        side.wait_stream(torch.cuda.current_stream())
+        a = ops.linear(x, w, activation="silu")
+        with torch.cuda.stream(side):
+            b = ops.linear(p["dout"], w, activation="gelu") + 0
+        torch.cuda.current_stream().wait_stream(side)
+        c = a + 0
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(c, want[0]) and torch.equal(b, want[1])
+    assert moe_mx.moe_mx_linear_status(0) == moe_mx.MOE_MX_OK
+
+
+def test_an_experts_weights_reach_its_own_rows_alone():
+    """NaN weights of two experts, one without rows, between others: sizes off every tile and block."""
+    E, N, K = 6, 66, 72
+    r = ref.make_routing(150, E, 2, 75)
+    x, w, b, _, _ = _linear_inputs(r.rows, N, K, BF, BF, "none", True, False, 76, E)
+    want = ops.linear(x, w, b, routing=r)
+    dout = rnd((r.rows, N), BF, 77)
+    want_dx, _, _ = ops.linear_backward(dout, x, w, routing=r, weight_grad=False)
+    empty = E // 3  # without rows
+    bad = w.clone()
+    bad[empty], bad[4] = math.nan, math.nan
+    got = ops.linear(x, bad, b, routing=r)
+    got_dx, _, _ = ops.linear_backward(dout, x, bad, routing=r, weight_grad=False)
+    for e, lo, hi in ref.segments(r, r.rows):
+        if e == 4:
+            assert got[lo:hi].isnan().all() and got_dx[lo:hi].isnan().all()
+        else:
+            assert torch.equal(got[lo:hi], want[lo:hi]) and torch.equal(got_dx[lo:hi], want_dx[lo:hi])
+    # a NaN row of one expert's x and dout stays out of the other experts' gradients
+    want_dw, want_db = ops.linear_backward(dout, x, w, routing=r, bias_grad=True)[1:]
+    lo = int(r.pad_offsets[4])
+    x[lo], dout[lo] = math.nan, math.nan
+    dw, db = ops.linear_backward(dout, x, w, routing=r, bias_grad=True)[1:]
+    keep = [e for e in range(E) if e != 4]
+    assert torch.equal(dw[keep], want_dw[keep]) and torch.equal(db[keep], want_db[keep])
+    assert dw[4].isnan().all() and db[4].isnan().all()
+
+
+def test_1024_experts():
+    r = ref.make_routing(700, 1024, 3, 78)
+    x, w, b, _, _ = _linear_inputs(r.rows, 40, 64, BF, BF, "silu", True, False, 79, 1024)
+    _check_linear(x, w, b, None, "silu", BF, r)
+    _check_backward(rnd((r.rows, 40), BF, 80), x, w, rnd((r.rows, 40), BF, 81), "silu", r)
+
+
+def test_offsets_past_31_bits():
+    """Grouped buffers, outputs and weights of more than 2^31 elements: rows at the far end."""
+    T, k, H, E = 40000, 8, 7168, 16
+    g = torch.Generator().manual_seed(82)
+    ids = torch.argsort(torch.rand(T, E, generator=g), 1)[:, :k].cuda()
+    logits = torch.full((T, E), -4.0, device="cuda").scatter_(1, ids, torch.arange(k, 0, -1, device="cuda").float().expand(T, k))
+    r = ops.route_group(logits, k)
+    assert r.rows * H > 2 ** 31
+    x = rnd((T, H), BF, 83)
+    y = ops.dispatch(x, r)
+    pos = r.pos_of_pair.long()
+    far = torch.topk(pos, 64).indices
+    assert int(pos[far].min()) * H > 2 ** 31 and torch.equal(y[pos[far]], x[far // k])
+    out = ops.combine(y, r)
+    dy, dw, _ = ops.combine_backward(x, y, r, num_experts=E)
+    tok = (far // k)[:8]
+    ref.close(out[tok], x[tok].to(ref.F64), x[tok].to(ref.F64).abs() * (k + 4) * 2.0 ** -23, "combine")
+    w = r.topk_w.reshape(-1)[far].to(ref.F64)[:, None]
+    ref.close(dy[pos[far]], x[far // k].to(ref.F64) * w, (x[far // k].to(ref.F64) * w).abs() * 2.0 ** -24, "dy")
+    sq = (x[tok].to(ref.F64) ** 2).sum(1, keepdim=True).expand(-1, k)
+    ref.close(dw[tok], sq, sq * (H + 2) * 2.0 ** -23, "dw")
+    del y, dy, out
+    M, N, K = 300000, 7200, 64
+    x, w = rnd((M, K), BF, 84), rnd((N, K), BF, 85)
+    got = ops.linear(x, w)
+    assert got.numel() > 2 ** 31
+    want, _, bound, _ = ref.linear64(x[-300:], w, None, None, "none")
+    ref.close(got[-300:], want, bound, "linear")
+    dx, dw, _ = ops.linear_backward(got, x, w)
+    (want, _, _), (bound, _, _) = ref.linear_backward64(got[-300:], x[-300:], w, None, "none")
+    ref.close(dx[-300:], want, bound, "dx")
+    del got, dx, dw
+    E, N, K = 9, 32768, 8192
+    r = ref.make_routing(20, E, 1, 86)
+    w = torch.zeros(E, N, K, dtype=BF, device="cuda")
+    assert w.numel() > 2 ** 31
+    last = int(r.counts.nonzero().max())
+    w[last, -64:] = rnd((64, K), BF, 87, K ** -0.5)
+    x = rnd((r.rows, K), BF, 88)
+    got = ops.linear(x, w, routing=r)
+    lo, n = int(r.pad_offsets[last]), int(r.counts[last])
+    want, _, bound, _ = ref.linear64(x[lo:lo + n], w[last, -64:].contiguous(), None, None, "none")
+    ref.close(got[lo:lo + n, -64:], want, bound, "grouped")
+    dout = rnd((r.rows, N), BF, 89)
+    dw = ops.linear_backward(dout, x, w, routing=r)[1]
+    want = dout[lo:lo + n, -64:].to(ref.F64).t() @ x[lo:lo + n].to(ref.F64)
+    ref.close(dw[last, -64:], want, (n + 2) * 2.0 ** -23 * (dout[lo:lo + n, -64:].to(ref.F64).abs().t() @ x[lo:lo + n].to(ref.F64).abs()), "grouped dw")
+
+
 def test_first_call_of_a_process_may_be_captured():
     code = """
 import torch

@@ -75,6 +75,11 @@ def test_workspace_covers_the_largest_calls(lib):
         assert lib.moe_mx_linear_backward_workspace(E, rows, N, K, 0, 1, 0) >= 2 * rows * N
 
 
+def test_status_refuses_a_device_that_is_not_there(lib):
+    assert lib.moe_mx_linear_status(-1, None) in (BAD, moe_mx.MOE_MX_ERR_CUDA)
+    assert lib.moe_mx_linear_status(1 << 20, None) in (BAD, moe_mx.MOE_MX_ERR_CUDA)
+
+
 def test_workspace_of_no_rows_is_no_error(lib):
     for E in (0, 4):
         assert lib.moe_mx_linear_workspace(E, 0, 32, 64, 0, 0, 0) >= 0
