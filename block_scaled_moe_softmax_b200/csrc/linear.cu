@@ -377,6 +377,31 @@ __device__ __forceinline__ void finish(const Epi &g, const Rows &w, float (&z)[R
     }
 }
 
+// Bias and activation of 64 columns of one row from column n.
+__device__ __forceinline__ void bias_act(const Epi &g, int n, uint32_t (&r0)[32], uint32_t (&r1)[32])
+{
+    if (g.bias) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            r0[i] = __float_as_uint(__uint_as_float(r0[i]) + (n + i < g.n_cols ? g.bias[n + i] : 0.f));
+            r1[i] = __float_as_uint(__uint_as_float(r1[i]) + (n + 32 + i < g.n_cols ? g.bias[n + 32 + i] : 0.f));
+        }
+    }
+    if (g.act == kActSilu) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            r0[i] = __float_as_uint(act_fwd(__uint_as_float(r0[i]), kActSilu));
+            r1[i] = __float_as_uint(act_fwd(__uint_as_float(r1[i]), kActSilu));
+        }
+    } else if (g.act == kActGelu) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            r0[i] = __float_as_uint(act_fwd(__uint_as_float(r0[i]), kActGelu));
+            r1[i] = __float_as_uint(act_fwd(__uint_as_float(r1[i]), kActGelu));
+        }
+    }
+}
+
 // The tensor core adds into its float32 accumulator by truncation: a chain over K = 7168 is off by
 // 8e-6 in relative norm (measured), where a rounding sum is by 9e-7.  Products with float32 outputs
 // therefore hand the accumulator over every kChain k blocks (kSum) and the epilogue's warps keep
@@ -421,6 +446,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto tile_full = [&](uint32_t r) { return bar0 + 8u * (2 * S + 5 + r); };
     auto tile_empty = [&](uint32_t r) { return bar0 + 8u * (2 * S + 5 + kRing + r); };
     int4 *const ring = reinterpret_cast<int4 *>(sm + C::kOffRing);
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    // A dense product's first tile depends on nothing in memory: found while the barriers are set up (its
+    // divisions and the first reads of the arguments take most of a microsecond)
+    Tile t;
+    const bool early = g.seg.E == 0;
+    bool some = early && get_tile<BN, kSwap, kMostTok>(g, nullptr, pair, t);
     int32_t *const prefix = reinterpret_cast<int32_t *>(sm + C::kOffPrefix); // kPrefix only
 
     if (threadIdx.x == 0) {
@@ -450,12 +481,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     grid_dep_launch(); // this CTA holds its TMEM: a kernel launched early cannot take it first
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + C::kOffBar + 8 * C::kNumBar);
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    Tile t;
     // The c-th tile of this pair (whole warp); false after the last, or if a wait gave up.
     auto next = [&](uint32_t &c) {
-        if (!kAhead)
-            return get_tile<BN, kSwap, kMostTok>(g, prefix, pair + (int)c++ * pairs, t);
+        if (!kAhead) { // dense: the first is found already
+            if (c > 0)
+                some = get_tile<BN, kSwap, kMostTok>(g, prefix, pair + (int)c * pairs, t);
+            ++c;
+            return some;
+        }
         const uint32_t r = c % kRing;
         if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(tile_full(r), (c / kRing) & 1, &g_linear_err, kWaitNs)))
             return false;
@@ -474,7 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp == 0 || (kSplit && warp == 2)) {
         // ------------------------------------------------------------ copies: A, and B
-        uint32_t it = 0; // k blocks issued
+        uint32_t it = 0, stage = 0, phase = 1; // k blocks issued, and the next one's stage and (inverted) phase
         while (ok && next(c)) {
             const int a_row = t.row + (int)rank * 128; // kSwap: weight rows (columns of D) from n0
             const int w_row = t.n0 + (int)rank * (g.gated ? 64 : 128), tok0 = t.row + (int)rank * (t.tok / 2);
@@ -484,55 +517,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int box_log = t.tok > 128 ? 3 : t.tok > 64 ? 2 : t.tok > 32 ? 1 : 0;
             const uint32_t bytes = C::kABytes + (kSwap ? 2048u << box_log : C::kBBytes);
             const int b_row = g.gated ? (int)rank * g.n_cols + t.n0 : t.n0 + (int)rank * (BN / 2);
-            for (int kb = 0; kb < t.nkb; ++kb, ++it) {
-                const int s = it % S;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty(s), ((it / S) & 1) ^ 1, &g_linear_err, kWaitNs))) {
+            auto copy = [&](int kb, uint32_t s) {
+                const int k = t.k0 + kb * kBk;
+                const uint32_t bar = map_rank(full(s), 0);
+                // the last block of a segment whose rows end inside it: its copy filled up with zeros
+                const bool cut = kAMn && kBMn && t.rem && kb == t.nkb - 1;
+                const int kr = cut ? t.e * kBk : k;
+                const uint32_t sa = base + s * C::kStage, sb = sa + C::kABytes;
+                if (!kSplit || warp == 0) {
+                    if (kAMn) {
+                        const CUtensorMap *m = !kSwap && cut ? &map_c.m[0] : &map_a;
+                        const int row = kSwap ? w_row : a_row, e = kSwap ? t.e : 0;
+                        if (g.wide_a)
+                            tma_pair_4d(sa, m, 0, kr, row / 64, e, bar);
+                        else
+                            for (int j = 0; j < 2; ++j)
+                                tma_pair_3d(sa + j * 8192, m, row + j * 64, kr, e, bar);
+                    } else if (kSwap && g.gated) {
+                        tma_pair_5d(sa, &map_a, k, 0, 0, w_row / 16, t.e, bar);
+                    } else if (kSwap) {
+                        tma_pair_3d(sa, &map_a, k, w_row, t.e, bar);
+                    } else {
+                        tma_pair_2d(sa, &map_a, k, a_row, bar);
+                    }
+                }
+                if (kSplit && warp == 0) {
+                } else if (kSwap) {
+                    tma_pair_2d(sb, box_log == 3 ? &map_b : &map_c.m[box_log], k, tok0, bar);
+                } else if (kBMn) {
+                    const CUtensorMap *m = cut ? &map_c.m[1] : &map_b;
+                    const int e = g.seg_k ? 0 : t.e;
+                    if (g.wide_b)
+                        tma_pair_4d(sb, m, 0, kr, b_row / 64, e, bar);
+                    else
+                        for (int j = 0; j < BN / 128; ++j)
+                            tma_pair_3d(sb + j * 8192, m, b_row + j * 64, kr, e, bar);
+                } else {
+                    tma_pair_3d(sb, &map_b, k, b_row, t.e, bar);
+                }
+            };
+            // A round of waits and copies takes the warp about 460 cycles: longer than the MMAs of a block of
+            // 128 columns, whose blocks are therefore taken two at a time (512 x 4096 -> 4096 22.1 -> 18.6 us).
+            // Wider tiles keep the second stage's copy in flight instead (8192 x 7168 -> 384 in 192 columns
+            // 49 us one at a time, 53 us two).
+            constexpr int kRound = BN == 128 ? 2 : 1;
+            for (int kb = 0; kb < t.nkb; kb += kRound) {
+                const bool two = kRound == 2 && kb + 1 < t.nkb;
+                const uint32_t s0 = stage, p0 = phase;
+                uint32_t s1 = s0 + 1, p1 = p0;
+                if (s1 == S)
+                    s1 = 0, p1 ^= 1;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty(s0), p0, &g_linear_err, kWaitNs) &&
+                                                 (!two || mbar_wait_bounded(empty(s1), p1, &g_linear_err, kWaitNs)))) {
                     ok = false;
                     break;
                 }
-                if (lane == 0) {
-                    const int k = t.k0 + kb * kBk;
-                    const uint32_t bar = map_rank(full(s), 0);
+                if (elect_lane()) {
                     // one arrival for both operands; B's bytes may land before it, which the barrier counts
-                    if (warp == 0)
-                        mbar_arrive_expect_tx_relaxed(bar, bytes);
-                    // the last block of a segment whose rows end inside it: its copy filled up with zeros
-                    const bool cut = kAMn && kBMn && t.rem && kb == t.nkb - 1;
-                    const int kr = cut ? t.e * kBk : k;
-                    const uint32_t sa = base + s * C::kStage, sb = sa + C::kABytes;
-                    if (!kSplit || warp == 0) {
-                        if (kAMn) {
-                            const CUtensorMap *m = !kSwap && cut ? &map_c.m[0] : &map_a;
-                            const int row = kSwap ? w_row : a_row, e = kSwap ? t.e : 0;
-                            if (g.wide_a)
-                                tma_pair_4d(sa, m, 0, kr, row / 64, e, bar);
-                            else
-                                for (int j = 0; j < 2; ++j)
-                                    tma_pair_3d(sa + j * 8192, m, row + j * 64, kr, e, bar);
-                        } else if (kSwap && g.gated) {
-                            tma_pair_5d(sa, &map_a, k, 0, 0, w_row / 16, t.e, bar);
-                        } else if (kSwap) {
-                            tma_pair_3d(sa, &map_a, k, w_row, t.e, bar);
-                        } else {
-                            tma_pair_2d(sa, &map_a, k, a_row, bar);
-                        }
+                    if (warp == 0) {
+                        mbar_arrive_expect_tx_relaxed(map_rank(full(s0), 0), bytes);
+                        if (two)
+                            mbar_arrive_expect_tx_relaxed(map_rank(full(s1), 0), bytes);
                     }
-                    if (kSplit && warp == 0) {
-                    } else if (kSwap) {
-                        tma_pair_2d(sb, box_log == 3 ? &map_b : &map_c.m[box_log], k, tok0, bar);
-                    } else if (kBMn) {
-                        const CUtensorMap *m = cut ? &map_c.m[1] : &map_b;
-                        const int e = g.seg_k ? 0 : t.e;
-                        if (g.wide_b)
-                            tma_pair_4d(sb, m, 0, kr, b_row / 64, e, bar);
-                        else
-                            for (int j = 0; j < BN / 128; ++j)
-                                tma_pair_3d(sb + j * 8192, m, b_row + j * 64, kr, e, bar);
-                    } else {
-                        tma_pair_3d(sb, &map_b, k, b_row, t.e, bar);
-                    }
+                    copy(kb, s0);
+                    if (two)
+                        copy(kb + 1, s1);
                 }
                 __syncwarp();
+                stage = two ? s1 + 1 : s1, phase = p1;
+                if (two && stage == S)
+                    stage = 0, phase ^= 1;
+                it += two ? 2 : 1;
             }
         }
         // Before either CTA may exit, every copy has landed (all report to the leader's barriers; a wait
@@ -578,7 +633,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         bool more = true;
         for (int i = pair; more; i += pairs, ++c) {
-            more = get_tile<BN, kSwap, kMostTok>(g, prefix, i, t);
+            more = early && c == 0 ? some : get_tile<BN, kSwap, kMostTok>(g, prefix, i, t);
             const uint32_t r = c % kRing;
             if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(tile_empty(r), ((c / kRing) & 1) ^ 1, &g_linear_err, kWaitNs)))
                 break;
@@ -592,7 +647,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------------ MMAs
-        uint32_t it = 0, n = 0;
+        uint32_t n = 0, stage = 0, phase = 0;
+        const uint64_t da0 = kAMn ? smem_desc_mn_sw128(base, 8192) : smem_desc_sw128(base);
+        const uint64_t db0 = kBMn ? smem_desc_mn_sw128(base + C::kABytes, 8192) : smem_desc_sw128(base + C::kABytes);
         while (ok && next(c)) {
             const uint32_t idesc = idesc_f16(g.fmt, kAMn, kBMn, kTileM, kSwap ? t.tok : BN);
             for (int kb = 0; ok && kb < t.nkb;) {
@@ -604,27 +661,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ++n;
                 tc_fence_after();
                 const int first = kb, end = kSum ? min(t.nkb, kb + kChain) : t.nkb;
-                for (; kb < end; ++kb, ++it) {
-                    const int s = it % S;
-                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(full(s), (it / S) & 1, &g_linear_err, kWaitNs))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (elect_lane()) {
-                        const uint32_t sa = base + s * C::kStage, sb = sa + C::kABytes;
-                        const uint64_t da = kAMn ? smem_desc_mn_sw128(sa, 8192) : smem_desc_sw128(sa);
-                        const uint64_t db = kBMn ? smem_desc_mn_sw128(sb, 8192) : smem_desc_sw128(sb);
-                        // 16 of k: 32 bytes of a K-major row, or two 1024-byte groups of 8 k
+                while (ok && kb < end) {
+                    // unrolled over the stages, whose descriptors are then constants apart (about 100 cycles less
+                    // a block; descriptors are affine in the address, which stays below 2^18)
 #pragma unroll
-                        for (int q = 0; q < kBk / 16; ++q)
-                            umma_f16_pair(tmem + 256u * buf, da + q * (kAMn ? 128 : 2), db + q * (kBMn ? 128 : 2),
-                                          idesc, kb > first || q > 0);
-                        umma_commit_pair(empty(s));
-                        if (kb == end - 1)
-                            umma_commit_pair(acc_full(buf));
+                    for (int s = 0; s < S; ++s) {
+                        if (s != (int)stage || kb >= end)
+                            continue;
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(full(s), phase, &g_linear_err, kWaitNs))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (elect_lane()) {
+                            // 16 of k: 32 bytes of a K-major row, or two 1024-byte groups of 8 k
+#pragma unroll
+                            for (int q = 0; q < kBk / 16; ++q)
+                                umma_f16_pair(tmem + 256u * buf, da0 + (s * (C::kStage >> 4) + q * (kAMn ? 128 : 2)),
+                                              db0 + (s * (C::kStage >> 4) + q * (kBMn ? 128 : 2)), idesc,
+                                              kb > first || q > 0);
+                            umma_commit_pair(empty(s));
+                            if (kb == end - 1)
+                                umma_commit_pair(acc_full(buf));
+                        }
+                        __syncwarp();
+                        ++kb;
+                        ++stage;
                     }
-                    __syncwarp();
+                    if (stage == S)
+                        stage = 0, phase ^= 1;
                 }
             }
         }
@@ -862,10 +927,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             } else {
-                if (kPlain && g.vec && g.out_type != kTypeF32 && cols % 64 == 0) {
-                    // A gradient: rounded where it lies (lane: row), turned 64 columns at a time as 16-bit
-                    // values, stored as whole 128-byte lines.  Half the shared-memory traffic of float32
-                    // blocks of 32 columns; gradients have short k, and this is what bounds them.
+                if (ep.vec && ep.out_type != kTypeF32 && cols % 64 == 0 && !ep.residual && !ep.preact &&
+                    (kPlain || !g.gated)) {
+                    // One 16-bit output: bias, activation and rounding where the values lie (lane: row), turned
+                    // 64 columns at a time as 16-bit values, stored as whole 128-byte lines.  Half the
+                    // shared-memory traffic of float32 blocks of 32 columns; it bounds products of short k, such
+                    // as gradients, and is what a single wave waits for at its end.
                     if (t.nkb > 0 && !wait_acc())
                         break;
                     uint4 *const line = reinterpret_cast<uint4 *>(stg);
@@ -881,6 +948,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             if (c + 64 >= cols)
                                 free_acc();
                         }
+                        if (!kPlain)
+                            bias_act(ep, t.n0 + lc, r0, r1);
                         auto pack = [&](auto zero) {
                             using T = decltype(zero);
 #pragma unroll
