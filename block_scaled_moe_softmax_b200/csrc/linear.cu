@@ -1347,8 +1347,10 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(const SmallArgs
         cluster_sync(); // the other CTAs' shared memory is read until here
 }
 
-// Whether a dense product runs as small_kernel: up to 16 rows, and rows of w of whole 16 bytes.
-bool is_small(int64_t M, int K) { return M <= kSmallRows && K % 8 == 0; }
+// Whether a dense product runs as small_kernel: up to 16 rows, rows of w of whole 16 bytes, and less than
+// 48 M weights.  Larger ones stream faster through the tile product with 32 tokens a tile: 16 rows by 4096 ->
+// 14336 (59 M) 35 us here and 25 us there, 8 rows by 4096 -> 8192 (34 M) 14 us here and 17 us there.
+bool is_small(int64_t M, int64_t N, int K) { return M <= kSmallRows && K % 8 == 0 && N * K < 48000000; }
 
 int launch_small(const SmallArgs &args, int type, cudaStream_t s)
 {
@@ -1357,9 +1359,12 @@ int launch_small(const SmallArgs &args, int type, cudaStream_t s)
     // 32 weight rows a CTA halve the reads of x; 16 where that leaves SMs without a CTA
     const bool two = gated || a.N >= 32 * 296;
     const int tiles = (a.epi.n_cols + (two && !gated ? 31 : 15)) / (two && !gated ? 32 : 16);
-    // k is shared by the CTAs of a cluster until there are two to four CTAs an SM, each warp keeping 64 elements
+    // k is shared by the CTAs of a cluster as long as all CTAs are resident at once (their registers allow two
+    // to four an SM) and each warp keeps 64 elements: 8 rows of 7168 -> 4096 with SwiGLU 15.5 us as 256
+    // CTAs, 18 as 512, of which 444 are resident
+    const int resident = 2 * kPairs * ((two ? 3 : 4) - (a.M > 8));
     int ranks = 1;
-    while (ranks < kMaxCluster && tiles * ranks <= 4 * kPairs && a.K >= 64 * kSmallWarps * ranks * 2)
+    while (ranks < kMaxCluster && tiles * ranks * 2 <= resident && a.K >= 64 * kSmallWarps * ranks * 2)
         ranks *= 2;
     a.k_warp = (int)round_up((a.K + kSmallWarps * ranks - 1) / (kSmallWarps * ranks), 32);
     cudaLaunchConfig_t cfg = {};
@@ -1661,7 +1666,7 @@ struct ForwardPlan {
 ForwardPlan plan_linear(int E, int64_t M, int N, int K, int act, bool f32)
 {
     ForwardPlan f{};
-    if (E == 0 && is_small(M, K))
+    if (E == 0 && is_small(M, N, K))
         return f;
     const bool gated = act == kActSwiglu;
     const bool swap = !gated || N % 32 == 0; // gate and up rows are taken 16 by 16
@@ -1753,7 +1758,7 @@ int64_t linear_backward_workspace(int E, int64_t M, int N, int K, int act, int t
 
 int launch_linear(const LinearArgs &a, cudaStream_t s)
 {
-    if (a.E == 0 && is_small(a.M, a.K)) {
+    if (a.E == 0 && is_small(a.M, a.N, a.K)) {
         const SmallArgs m{a.x, a.w, (int)a.M, a.N, a.K, 0,
                           Epi{a.bias, a.residual, a.out, a.preact, a.act, a.N, a.No(), a.type, a.out_type, 0}};
         return launch_small(m, a.type, s);

@@ -201,6 +201,12 @@ def test_linear_few_rows(M, N, K, act, bias, residual, dtype, out):
     _check_linear(x, w, b, res, act, out)
 
 
+def test_linear_few_rows_of_large_weights():
+    """More weights than the few-row kernel takes: tiles of 32 tokens."""
+    x, w, b, _, _ = _linear_inputs(9, 14400, 4096, BF, BF, "swiglu", True, False, 90)
+    _check_linear(x, w, b, None, "swiglu", BF)
+
+
 @pytest.mark.parametrize("M,N,K,act", [(1000, 384, 7168, "none"), (300, 264, 3000, "none"), (520, 256, 2048, "swiglu"),
                                        (40, 400, 7168, "silu"), (600, 34, 1040, "swiglu")])
 def test_linear_float32_outputs_keep_their_precision(M, N, K, act):
