@@ -12,7 +12,7 @@ gradients (the ``moe_mx_*`` entry points of the same names in include/moe_mx.h).
     dg, dw1, _ = linear_backward(dh, g, w1, preact=z, activation="swiglu", routing=r)
     dx = dispatch_backward(dg, r)
 
-Gradients are explicit calls, as everything in the library is.  Tensors are contiguous CUDA tensors of
+Gradients are explicit calls, as everything in the library is: results carry no autograd history.  Tensors are contiguous CUDA tensors of
 one device; a call is enqueued on ``stream`` (a torch.cuda.Stream or a raw handle; default: the current
 stream of the tensors' device) and allocates only what it returns and its workspace, from torch's
 allocator, as under ``with torch.cuda.stream(stream)``.  Wrong types, shapes or
@@ -44,11 +44,11 @@ class Routing(NamedTuple):
     rows: int                  # rows of the grouped buffers
 
 
-def _tensor(t, name, like, dtype=None, shape=None):
-    """t, checked: a contiguous tensor on the device of ``like``, of the given type and shape."""
-    # one test for the usual case: these checks are most of a small call's time on the host
+def _tensor(t, name, device, dtype=None, shape=None):
+    """t, checked: a contiguous tensor on CUDA device number ``device``, of the given type and shape."""
+    # one test for the usual case: these checks are a good part of a small call's time on the host
     if (isinstance(t, torch.Tensor) and (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)
-            and t.is_contiguous() and t.get_device() == like.get_device()):
+            and t.is_contiguous() and t.get_device() == device):
         return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
@@ -58,7 +58,14 @@ def _tensor(t, name, like, dtype=None, shape=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    raise ValueError(f"{name} is on {t.device}, not {like.device}")
+    raise ValueError(f"{name} is on {t.device}, not on {'the CPU' if device < 0 else f'cuda:{device}'}")
+
+
+def _device(t, name):
+    """The number of t's CUDA device (-1 for a CPU tensor, which _on refuses)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    return t.get_device()
 
 
 def _type(t, name):
@@ -68,12 +75,12 @@ def _type(t, name):
     return code
 
 
-def _on(t, stream):
+def _on(t, device, stream):
     """The raw handle of the stream of a call on t's device."""
-    if not t.is_cuda:
+    if device < 0:
         raise ValueError(f"tensors must be on a CUDA device, not {t.device}")
     if stream is None:
-        return _raw_stream(t.get_device())
+        return _raw_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -86,42 +93,42 @@ def _empty(shape, dtype, like, stream):
     """A new tensor of the call's stream: on another stream than the current one it comes from that
     stream's pool, since memory freed on the current stream may still be in use there."""
     if stream is None:
-        return like.new_empty(*shape, dtype=dtype)
+        return like.new_empty(*shape) if dtype is like.dtype else like.new_empty(*shape, dtype=dtype)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=like.device)
     with torch.cuda.stream(stream):
         return like.new_empty(*shape, dtype=dtype)
 
 
-def _pairs(r: Routing, like):
+def _pairs(r: Routing, device):
+    """(tokens, slots) of a routing whose weights and rows are checked."""
+    _tensor(r.topk_w, "topk_w", device, torch.float32)
     shape = r.topk_w.shape
-    _tensor(r.topk_w, "topk_w", like, torch.float32)
     if len(shape) != 2:
         raise ValueError("topk_w must be [tokens, slots]")
     T, k = shape
-    _tensor(r.pos_of_pair, "pos_of_pair", like, torch.int32, (T * k,))
+    _tensor(r.pos_of_pair, "pos_of_pair", device, torch.int32, (T * k,))
     return T, k
 
 
-def _matrix(t, name, like, rows=None, dtype=None):
+def _matrix(t, name, device, rows=None, dtype=None):
     """t as a checked [rows, columns] matrix; its columns."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not [{'rows' if rows is None else rows}, columns]")
-    _tensor(t, name, like, dtype)
-    return t.shape[1]
+    shape = t.shape if isinstance(t, torch.Tensor) else None
+    if shape is not None and (len(shape) != 2 or (rows is not None and shape[0] != rows)):
+        raise ValueError(f"{name} has shape {tuple(shape)}, not [{'rows' if rows is None else rows}, columns]")
+    _tensor(t, name, device, dtype)
+    return shape[1]
 
 
-def _out(out, shape, dtype, like, name, stream):
+def _out(out, shape, dtype, like, device, name, stream):
     if out is None:
         return _empty(shape, dtype, like, stream)
-    return _tensor(out, name, like, dtype, shape)
+    return _tensor(out, name, device, dtype, shape)
 
 
 def _call(name, *args):
     """The entry point of that name on raw arguments; raises MoeMxError."""
-    code = getattr(moe_mx.load_library(), name)(*args)
+    code = getattr(moe_mx._lib or moe_mx.load_library(), name)(*args)
     if code:
         raise moe_mx.MoeMxError(code, moe_mx.moe_mx_last_error())
 
@@ -143,9 +150,10 @@ def max_grouped_rows(pairs: int, num_experts: int) -> int:
 def route_group(router_logits: torch.Tensor, top_k: int, stream=None) -> Routing:
     """Softmax top-k routing of float32 logits [T, E] and the grouped layout of the pairs
     (moe_mx_route_group_noalloc, whose calls on one device share a scratch: order them)."""
-    E = _matrix(router_logits, "router_logits", router_logits, dtype=torch.float32)
+    dev = _device(router_logits, "router_logits")
+    E = _matrix(router_logits, "router_logits", dev, dtype=torch.float32)
     T = router_logits.shape[0]
-    on = _on(router_logits, stream)
+    on = _on(router_logits, dev, stream)
     rows = max_grouped_rows(T * top_k, E)
     new = lambda *shape, dtype=torch.int32: _empty(shape, dtype, router_logits, stream)  # noqa: E731
     ids, w = new(T, top_k), new(T, top_k, dtype=torch.float32)
@@ -153,31 +161,33 @@ def route_group(router_logits: torch.Tensor, top_k: int, stream=None) -> Routing
     if T == 0:
         counts.zero_()
         pad.zero_()
-    with torch.cuda.device(router_logits.device):
+    with torch.cuda.device(dev):
         moe_mx.moe_mx_route_group_noalloc(router_logits, T, E, top_k, ids, w, counts, pad, pair, pos, on)
     return Routing(ids, w, counts, pad, pos, rows)
 
 
 def dispatch(x: torch.Tensor, routing: Routing, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Token rows x [T, H] at their pairs' grouped rows: [rows, H]; padding rows are not written."""
-    T, k = _pairs(routing, x)
-    H = _matrix(x, "x", x, T)
-    on = _on(x, stream)
+    dev = _device(x, "x")
+    T, k = _pairs(routing, dev)
+    H = _matrix(x, "x", dev, T)
+    on = _on(x, dev, stream)
     code = _type(x, "x")
-    out = _out(out, (routing.rows, H), x.dtype, x, "out", stream)
+    out = _out(out, (routing.rows, H), x.dtype, x, dev, "out", stream)
     _call("moe_mx_dispatch", x.data_ptr(), T, H, k, routing.pos_of_pair.data_ptr(), routing.rows, code, out.data_ptr(),
           on)
     return out
 
 
 def _combine(grouped, routing, w, out_dtype, out, stream):
-    T, k = _pairs(routing, grouped)
-    H = _matrix(grouped, "grouped", grouped, routing.rows)
-    on = _on(grouped, stream)
+    dev = _device(grouped, "grouped")
+    T, k = _pairs(routing, dev)
+    H = _matrix(grouped, "grouped", dev, routing.rows)
+    on = _on(grouped, dev, stream)
+    code = _type(grouped, "grouped")
     if out is not None:
         out_dtype = out.dtype
-    code = _type(grouped, "grouped")
-    out = _out(out, (T, H), out_dtype or grouped.dtype, grouped, "out", stream)
+    out = _out(out, (T, H), out_dtype or grouped.dtype, grouped, dev, "out", stream)
     _call("moe_mx_combine", grouped.data_ptr(), routing.rows, T, H, k, routing.pos_of_pair.data_ptr(), _ptr(w), code,
           _type(out, "out"), out.data_ptr(), on)
     return out
@@ -199,44 +209,47 @@ def combine_backward(dout: torch.Tensor, grouped: torch.Tensor, routing: Routing
                      dy: torch.Tensor | None = None, stream=None):
     """Gradient of combine: (dgrouped [rows, H], dtopk_w [T, k], dlogits [T, num_experts] or None when
     num_experts is 0).  dlogits is the gradient through the router's softmax over the chosen logits."""
-    T, k = _pairs(routing, dout)
-    H = _matrix(dout, "dout", dout, T)
-    _tensor(grouped, "grouped", dout, shape=(routing.rows, H))
-    on = _on(dout, stream)
+    dev = _device(dout, "dout")
+    T, k = _pairs(routing, dev)
+    H = _matrix(dout, "dout", dev, T)
+    _tensor(grouped, "grouped", dev, None, (routing.rows, H))
+    on = _on(dout, dev, stream)
     code, dout_code = _type(grouped, "grouped"), _type(dout, "dout")
-    dy = _out(dy, (routing.rows, H), grouped.dtype, dout, "dy", stream)
-    dw = _empty((T, k), torch.float32, dout, stream)
+    dy = _out(dy, (routing.rows, H), grouped.dtype, dout, dev, "dy", stream)
+    w = routing.topk_w
+    dw = _empty((T, k), torch.float32, w, stream)
     ids = dlogits = None
     if num_experts:
-        ids = _tensor(routing.topk_ids, "topk_ids", dout, torch.int32, (T, k))
-        dlogits = _empty((T, num_experts), torch.float32, dout, stream)
+        ids = _tensor(routing.topk_ids, "topk_ids", dev, torch.int32, (T, k))
+        dlogits = _empty((T, num_experts), torch.float32, w, stream)
     _call("moe_mx_combine_backward", dout.data_ptr(), grouped.data_ptr(), routing.rows, T, H, k,
-          routing.pos_of_pair.data_ptr(), routing.topk_w.data_ptr(), _ptr(ids), num_experts, code, dout_code,
-          dy.data_ptr(), dw.data_ptr(), _ptr(dlogits), on)
+          routing.pos_of_pair.data_ptr(), w.data_ptr(), _ptr(ids), num_experts, code, dout_code, dy.data_ptr(),
+          dw.data_ptr(), _ptr(dlogits), on)
     return dy, dw, dlogits
 
 
-def _linear_sizes(x, w, activation, routing):
+def _linear_sizes(x, w, activation, routing, dev):
     """(experts, rows, N, K, activation, columns of out, counts, pad_offsets) of a linear call, its operands
     checked; raw pointers for the last two."""
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation {activation!r} is not one of {', '.join(ACTIVATIONS)}")
-    K = _matrix(x, "x", x)
+    K = _matrix(x, "x", dev)
     if x.dtype is not torch.bfloat16 and x.dtype is not torch.float16:
         raise TypeError(f"x has type {x.dtype}; bfloat16 and float16 are supported")
-    _tensor(w, "w", x, x.dtype)
+    _tensor(w, "w", dev, x.dtype)
     E = 0 if routing is None else routing.counts.shape[0]
-    if w.dim() != (3 if E else 2) or w.shape[-1] != K or (E and w.shape[0] != E):
-        raise ValueError(f"x {tuple(x.shape)} and w {tuple(w.shape)}: need [rows, K] and "
+    shape = w.shape
+    if len(shape) != (3 if E else 2) or shape[-1] != K or (E and shape[0] != E):
+        raise ValueError(f"x {tuple(x.shape)} and w {tuple(shape)}: need [rows, K] and "
                          + (f"[{E}, N, K]" if E else "[N, K]"))
-    rows, N = x.shape[0], w.shape[-2]
+    rows, N = x.shape[0], shape[-2]
     counts = pad = None
     if E:
         if rows != routing.rows:
             raise ValueError(f"x has {rows} rows, the grouped layout {routing.rows}")
-        counts = _tensor(routing.counts, "counts", x, torch.int32, (E,)).data_ptr()
-        pad = _tensor(routing.pad_offsets, "pad_offsets", x, torch.int32, (E + 1,)).data_ptr()
+        counts = _tensor(routing.counts, "counts", dev, torch.int32, (E,)).data_ptr()
+        pad = _tensor(routing.pad_offsets, "pad_offsets", dev, torch.int32, (E + 1,)).data_ptr()
     cols = N
     if activation == "swiglu":
         if N % 2:
@@ -253,19 +266,20 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
     rows are grouped, w [E, N, K] and bias [E, N].  out and residual: [rows, N] ([rows, N/2] for
     swiglu) of x's type or float32; residual may be out itself.  A ``preact`` buffer [rows, N] receives
     x w^T + bias for linear_backward."""
-    E, rows, N, K, act, cols, counts, pad = _linear_sizes(x, w, activation, routing)
-    on = _on(x, stream)
+    dev = _device(x, "x")
+    E, rows, N, K, act, cols, counts, pad = _linear_sizes(x, w, activation, routing, dev)
+    on = _on(x, dev, stream)
     if bias is not None:
-        _tensor(bias, "bias", x, torch.float32, (E, N) if E else (N,))
+        _tensor(bias, "bias", dev, torch.float32, (E, N) if E else (N,))
     if out is not None:
         out_dtype = out.dtype
     elif out_dtype is None:
         out_dtype = x.dtype if residual is None else residual.dtype
-    out = _out(out, (rows, cols), out_dtype, x, "out", stream)
+    out = _out(out, (rows, cols), out_dtype, x, dev, "out", stream)
     if residual is not None:
-        _tensor(residual, "residual", x, out_dtype, (rows, cols))
+        _tensor(residual, "residual", dev, out_dtype, (rows, cols))
     if preact is not None:
-        _tensor(preact, "preact", x, x.dtype, (rows, N))
+        _tensor(preact, "preact", dev, x.dtype, (rows, N))
     dt, ot = _type(x, "x"), _type(out, "out")
     need = _linear_workspace(E, rows, N, K, dt, act, ot)
     ws = _empty((need,), torch.uint8, x, stream) if need else None
@@ -280,18 +294,19 @@ def linear_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, preact
                     dw: torch.Tensor | None = None, stream=None):
     """Gradient of linear: (dx, dw, dbias), None for those not asked for.  dout is of x's type or float32;
     preact as linear wrote it (for an activation).  The residual's gradient is dout."""
-    E, rows, N, K, act, cols, counts, pad = _linear_sizes(x, w, activation, routing)
-    on = _on(x, stream)
-    _tensor(dout, "dout", x, shape=(rows, cols))
+    dev = _device(x, "x")
+    E, rows, N, K, act, cols, counts, pad = _linear_sizes(x, w, activation, routing, dev)
+    on = _on(x, dev, stream)
+    _tensor(dout, "dout", dev, None, (rows, cols))
     if act:
-        _tensor(preact, "preact", x, x.dtype, (rows, N))
+        _tensor(preact, "preact", dev, x.dtype, (rows, N))
     elif preact is not None:
         raise ValueError("preact is taken with an activation only")
     if not (input_grad or weight_grad or bias_grad):
         raise ValueError("no gradient is asked for")
     dt, gt = _type(x, "x"), _type(dout, "dout")
-    dx = _out(dx, (rows, K), x.dtype, x, "dx", stream) if input_grad else None
-    dw = _out(dw, w.shape, x.dtype, x, "dw", stream) if weight_grad else None
+    dx = _out(dx, (rows, K), x.dtype, x, dev, "dx", stream) if input_grad else None
+    dw = _out(dw, w.shape, x.dtype, x, dev, "dw", stream) if weight_grad else None
     db = _empty((E, N) if E else (N,), torch.float32, x, stream) if bias_grad else None
     need = _linear_backward_workspace(E, rows, N, K, dt, act, gt)
     ws = _empty((need,), torch.uint8, x, stream) if need else None
