@@ -1201,14 +1201,14 @@ Plan plan_dense(int64_t M, int cols, int kb, bool gated, bool mn, bool f32, bool
 }
 
 // ---------------------------------------------------------------- a few rows
-// Up to 16 rows of x (one decode step): the product streams w once and its time is w's bytes over the
+// A few rows of x (a decode step): the product streams w once and its time is w's bytes over the
 // memory rate, or launch latency.  Weight rows are the A operand of 16 x 8 x 16 warp MMAs, tokens the
 // B operand; a warp takes kR x 16 weight rows over a slice of k, the 8 warps of a CTA and the CTAs of a
 // cluster share k, and the partial sums meet in shared memory (a fixed order, one launch, where
 // a split tile product writes planes and launches a second kernel: 16.7 -> 8.6 us a call of
 // 384 x 7168, most of it the host's).  Within a 32-element k block lane t of a row's four holds elements
 // 8t .. 8t + 7 of both operands (one 16-byte load), which the two MMAs take in the same order.
-constexpr int kSmallRows = 16, kSmallWarps = 8, kMaxCluster = 8;
+constexpr int kSmallWarps = 8, kMaxCluster = 8;
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -1261,7 +1261,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(const SmallArgs
     }
     float acc[kR][kNb][4] = {};
     const int k0 = (int)(rank * kSmallWarps + warp) * a.k_warp, k1 = min(a.K, k0 + a.k_warp);
-    constexpr int kU = 4; // k blocks of 32 in flight
+    constexpr int kU = kNb <= 2 ? 4 : 2; // k blocks of 32 in flight
     for (int k = k0; k < k1; k += 32 * kU) {
         uint4 wv[kU][2 * kR], xv[kU][kNb];
 #pragma unroll
@@ -1347,22 +1347,29 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(const SmallArgs
         cluster_sync(); // the other CTAs' shared memory is read until here
 }
 
-// Whether a dense product runs as small_kernel: up to 16 rows, rows of w of whole 16 bytes, and less than
-// 48 M weights.  Larger ones stream faster through the tile product with 32 tokens a tile: 16 rows by 4096 ->
-// 14336 (59 M) 35 us here and 25 us there, 8 rows by 4096 -> 8192 (34 M) 14 us here and 17 us there.
-bool is_small(int64_t M, int64_t N, int K) { return M <= kSmallRows && K % 8 == 0 && N * K < 48000000; }
+// Whether a dense product runs as small_kernel: few rows, and rows of w of whole 16 bytes.
+// - Up to 16 rows: less than 48 M weights.  Larger ones stream faster through the tile product with 32 tokens a
+//   tile: 16 rows by 4096 -> 14336 (59 M) 35 us here and 25 us there, 8 rows by 4096 -> 8192 (34 M) 14 us
+//   here and 17 us there.
+// - Up to 64 rows (32 with SwiGLU, whose partial sums take twice the shared memory): less than 192 M
+//   multiplications, since every CTA reads its slice of all rows of x.  7168 -> 384: 17 rows 7.2 us here, 12.0 as
+//   split tiles, 64 rows 10.8 and 12.7; 64 rows by 4096 -> 1400 15.6 us here, 10.3 as tiles.
+bool is_small(int64_t M, int64_t N, int K, bool gated)
+{
+    return K % 8 == 0 && (M <= 16 ? N * K < 48000000 : M <= (gated ? 32 : 64) && M * N * K < 192000000);
+}
 
 int launch_small(const SmallArgs &args, int type, cudaStream_t s)
 {
     SmallArgs a = args;
     const bool gated = a.epi.act == kActSwiglu;
     // 32 weight rows a CTA halve the reads of x; 16 where that leaves SMs without a CTA
-    const bool two = gated || a.N >= 32 * 296;
+    const bool two = gated || (a.M <= 16 && a.N >= 32 * 296);
     const int tiles = (a.epi.n_cols + (two && !gated ? 31 : 15)) / (two && !gated ? 32 : 16);
-    // k is shared by the CTAs of a cluster as long as all CTAs are resident at once (their registers allow two
+    // k is shared by the CTAs of a cluster as long as all CTAs are resident at once (their registers allow one
     // to four an SM) and each warp keeps 64 elements: 8 rows of 7168 -> 4096 with SwiGLU 15.5 us as 256
     // CTAs, 18 as 512, of which 444 are resident
-    const int resident = 2 * kPairs * ((two ? 3 : 4) - (a.M > 8));
+    const int resident = 2 * kPairs * (a.M > 32 ? 1 : a.M > 16 ? 2 : (two ? 3 : 4) - (a.M > 8));
     int ranks = 1;
     while (ranks < kMaxCluster && tiles * ranks * 2 <= resident && a.K >= 64 * kSmallWarps * ranks * 2)
         ranks *= 2;
@@ -1382,13 +1389,15 @@ int launch_small(const SmallArgs &args, int type, cudaStream_t s)
     cudaError_t ce = cudaSuccess;
     by_half(type, [&](auto zero) {
         using T = decltype(zero);
-        const bool one = a.M <= 8;
-        if (gated)
-            ce = cudaLaunchKernelEx(&cfg, one ? small_kernel<T, 2, 1, true> : small_kernel<T, 2, 2, true>, a);
-        else if (two)
-            ce = cudaLaunchKernelEx(&cfg, one ? small_kernel<T, 2, 1, false> : small_kernel<T, 2, 2, false>, a);
-        else
-            ce = cudaLaunchKernelEx(&cfg, one ? small_kernel<T, 1, 1, false> : small_kernel<T, 1, 2, false>, a);
+        auto kernel = gated ? (a.M <= 8    ? small_kernel<T, 2, 1, true>
+                               : a.M <= 16 ? small_kernel<T, 2, 2, true>
+                                           : small_kernel<T, 2, 4, true>)
+                      : two ? (a.M <= 8 ? small_kernel<T, 2, 1, false> : small_kernel<T, 2, 2, false>)
+                            : (a.M <= 8    ? small_kernel<T, 1, 1, false>
+                               : a.M <= 16 ? small_kernel<T, 1, 2, false>
+                               : a.M <= 32 ? small_kernel<T, 1, 4, false>
+                                           : small_kernel<T, 1, 8, false>);
+        ce = cudaLaunchKernelEx(&cfg, kernel, a);
     });
     return ce == cudaSuccess ? MOE_MX_OK : cuda_fail(ce, "linear launch");
 }
@@ -1666,7 +1675,7 @@ struct ForwardPlan {
 ForwardPlan plan_linear(int E, int64_t M, int N, int K, int act, bool f32)
 {
     ForwardPlan f{};
-    if (E == 0 && is_small(M, N, K))
+    if (E == 0 && is_small(M, N, K, act == kActSwiglu))
         return f;
     const bool gated = act == kActSwiglu;
     const bool swap = !gated || N % 32 == 0; // gate and up rows are taken 16 by 16
@@ -1758,7 +1767,7 @@ int64_t linear_backward_workspace(int E, int64_t M, int N, int K, int act, int t
 
 int launch_linear(const LinearArgs &a, cudaStream_t s)
 {
-    if (a.E == 0 && is_small(a.M, a.N, a.K)) {
+    if (a.E == 0 && is_small(a.M, a.N, a.K, a.act == kActSwiglu)) {
         const SmallArgs m{a.x, a.w, (int)a.M, a.N, a.K, 0,
                           Epi{a.bias, a.residual, a.out, a.preact, a.act, a.N, a.No(), a.type, a.out_type, 0}};
         return launch_small(m, a.type, s);

@@ -187,9 +187,9 @@ def test_linear_dense(M, N, K, act, bias, residual, dtype, out):
     _check_linear(x, w, b, res, act, out)
 
 
-FEW = [  # up to 16 rows: one launch, k shared by warps and the CTAs of a cluster
+FEW = [  # few rows: one launch, k shared by warps and the CTAs of a cluster
     (1, 384, 7168), (3, 40, 7168), (9, 34, 4104), (16, 10000, 1000), (8, 9480, 264), (5, 16, 8), (13, 130, 24),
-    (16, 4096, 2056),
+    (16, 4096, 2056), (17, 384, 7168), (32, 130, 1000), (33, 258, 520), (64, 384, 7168), (50, 40, 72), (31, 1000, 2048),
 ]
 
 
