@@ -13,6 +13,8 @@
 #include "routed.cuh"
 #include "vec.cuh"
 
+#include <type_traits>
+
 namespace moe_mx {
 
 namespace {
@@ -1230,8 +1232,15 @@ struct SmallArgs {
     Epi epi;
 };
 
-// kR: 16-row weight tiles of a CTA (swiglu: a gate and an up tile); kNb: 8-token groups.
-template <typename T, int kR, int kNb, bool kGated>
+// kR: 16-row weight tiles of a CTA (swiglu: a gate and an up tile); kNb: 8-token groups; kShort: the MMAs
+// truncate their sums, as the tile product's do (kChain), so chains of 32 kU of k are summed by float32 adds.
+// For float32 outputs of more than kSmallChain of k a warp: 16 rows by 7168 -> 4096, 896 of k a warp, a
+// relative error of 8.6e-7 in one chain, 1.4e-7 in short ones, both 16 us (with SwiGLU, 8 rows: 8.4e-7 and
+// 2.5e-7, 15.4 us).  A 16-bit output's own rounding is larger by far; short chains everywhere cost 48 rows by
+// 1408 -> 2816 8.8 -> 12.7 us, in registers.
+constexpr int kSmallChain = 256;
+
+template <typename T, int kR, int kNb, bool kGated, bool kShort>
 __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(const SmallArgs a)
 {
     constexpr int kOut = kR * 16 * kNb * 8; // partial sums of a CTA: [weight row][token]
@@ -1261,6 +1270,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(const SmallArgs
     }
     float acc[kR][kNb][4] = {};
     const int k0 = (int)(rank * kSmallWarps + warp) * a.k_warp, k1 = min(a.K, k0 + a.k_warp);
+    float sum[kR][kNb][4] = {}; // kShort: of the chains before
     constexpr int kU = kNb <= 2 ? 4 : 2; // k blocks of 32 in flight
     for (int k = k0; k < k1; k += 32 * kU) {
         uint4 wv[kU][2 * kR], xv[kU][kNb];
@@ -1285,6 +1295,16 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(const SmallArgs
                     mma16816<T>(acc[r][b], lo.x, hi.x, lo.y, hi.y, v.x, v.y);
                     mma16816<T>(acc[r][b], lo.z, hi.z, lo.w, hi.w, v.z, v.w);
                 }
+        if (kShort)
+#pragma unroll
+            for (int r = 0; r < kR; ++r)
+#pragma unroll
+                for (int b = 0; b < kNb; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        sum[r][b][i] += acc[r][b][i];
+                        acc[r][b][i] = 0.f;
+                    }
     }
     // element (weight row 16 r + g (+ 8), token 8 b + 2 t (+ 1))
 #pragma unroll
@@ -1293,7 +1313,8 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(const SmallArgs
         for (int b = 0; b < kNb; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                part[warp][(r * 16 + g + (i >> 1) * 8) * (kNb * 8) + b * 8 + 2 * t + (i & 1)] = acc[r][b][i];
+                part[warp][(r * 16 + g + (i >> 1) * 8) * (kNb * 8) + b * 8 + 2 * t + (i & 1)] =
+                    kShort ? sum[r][b][i] + acc[r][b][i] : acc[r][b][i];
     __syncthreads();
     for (int i = threadIdx.x; i < kOut; i += kSmallWarps * 32) {
         float s = 0.f;
@@ -1389,14 +1410,19 @@ int launch_small(const SmallArgs &args, int type, cudaStream_t s)
     cudaError_t ce = cudaSuccess;
     by_half(type, [&](auto zero) {
         using T = decltype(zero);
-        auto kernel = gated ? (a.M <= 8    ? small_kernel<T, 2, 1, true>
-                               : a.M <= 16 ? small_kernel<T, 2, 2, true>
-                                           : small_kernel<T, 2, 4, true>)
-                      : two ? (a.M <= 8 ? small_kernel<T, 2, 1, false> : small_kernel<T, 2, 2, false>)
-                            : (a.M <= 8    ? small_kernel<T, 1, 1, false>
-                               : a.M <= 16 ? small_kernel<T, 1, 2, false>
-                               : a.M <= 32 ? small_kernel<T, 1, 4, false>
-                                           : small_kernel<T, 1, 8, false>);
+        auto pick = [&](auto is_short) {
+            constexpr bool kS = decltype(is_short)::value;
+            return gated ? (a.M <= 8    ? small_kernel<T, 2, 1, true, kS>
+                            : a.M <= 16 ? small_kernel<T, 2, 2, true, kS>
+                                        : small_kernel<T, 2, 4, true, kS>)
+                   : two ? (a.M <= 8 ? small_kernel<T, 2, 1, false, kS> : small_kernel<T, 2, 2, false, kS>)
+                         : (a.M <= 8    ? small_kernel<T, 1, 1, false, kS>
+                            : a.M <= 16 ? small_kernel<T, 1, 2, false, kS>
+                            : a.M <= 32 ? small_kernel<T, 1, 4, false, kS>
+                                        : small_kernel<T, 1, 8, false, kS>);
+        };
+        const bool is_short = a.epi.out_type == kTypeF32 && a.k_warp > kSmallChain;
+        auto kernel = is_short ? pick(std::true_type()) : pick(std::false_type());
         ce = cudaLaunchKernelEx(&cfg, kernel, a);
     });
     return ce == cudaSuccess ? MOE_MX_OK : cuda_fail(ce, "linear launch");

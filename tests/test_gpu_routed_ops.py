@@ -208,7 +208,8 @@ def test_linear_few_rows_of_large_weights():
 
 
 @pytest.mark.parametrize("M,N,K,act", [(1000, 384, 7168, "none"), (300, 264, 3000, "none"), (520, 256, 2048, "swiglu"),
-                                       (40, 400, 7168, "silu"), (600, 34, 1040, "swiglu")])
+                                       (40, 400, 7168, "silu"), (600, 34, 1040, "swiglu"), (16, 4096, 7168, "none"),
+                                       (9, 1000, 20000, "none"), (30, 200, 9000, "swiglu")])
 def test_linear_float32_outputs_keep_their_precision(M, N, K, act):
     """float32 outputs of long products.  The sum is kept in chains of 512 of k, 32 tensor-core additions that
     may truncate by 2^-23 of a running sum of norm sqrt(i / 32): 21.3 x 2^-23 = 2.5e-6 of a chain's norm at
