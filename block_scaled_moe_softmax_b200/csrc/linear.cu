@@ -264,7 +264,7 @@ template <int R> struct Ahead {
 template <typename T, int R>
 __device__ __forceinline__ void add_rows(const Epi &g, const Ahead<R> &ahead, const Rows &w, float (&v)[R][8])
 {
-    if (g.vec) {
+    if (R > 1 || g.vec) { // finish_column has the tiles' others
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             Raw<T, 8> r;
@@ -294,7 +294,7 @@ __device__ __forceinline__ void add_rows(const Epi &g, const Ahead<R> &ahead, co
 template <typename T, int R>
 __device__ __forceinline__ void put_rows(T *p, int step, const Epi &g, const Rows &w, const float (&v)[R][8])
 {
-    if (g.vec) {
+    if (R > 1 || g.vec) {
 #pragma unroll
         for (int j = 0; j < R; ++j)
             if (w.has(j))
@@ -377,6 +377,84 @@ __device__ __forceinline__ void finish(const Epi &g, const Rows &w, float (&z)[R
             add_rows<__nv_bfloat16, R>(g, ahead, w, z);
         put_rows<__nv_bfloat16, R>(static_cast<__nv_bfloat16 *>(g.out) + w.o, w.so, g, w, z);
     }
+}
+
+template <typename T>
+__device__ __forceinline__ void put_column(void *out, size_t off, int step, int rows, const float (&v)[32])
+{
+    T *p = static_cast<T *>(out) + off;
+#pragma unroll
+    for (int x = 0; x < 32; ++x, p += step)
+        if (x < rows)
+            *p = from_f32<T>(v[x]);
+}
+
+template <typename T> __device__ __forceinline__ void add_column(const void *res, size_t off, int step, int rows, float (&v)[32])
+{
+    const T *p = static_cast<const T *>(res) + off;
+#pragma unroll
+    for (int x = 0; x < 32; ++x, p += step)
+        if (x < rows)
+            v[x] += to_f32<T>(*p);
+}
+
+template <typename T>
+__device__ __forceinline__ void end_column(const Epi &g, size_t off, int rows, float (&v)[32])
+{
+    if (g.residual)
+        add_column<T>(g.residual, off, g.n_cols, rows, v);
+    put_column<T>(g.out, off, g.n_cols, rows, v);
+}
+
+// The same for outputs whose rows do not start on 16 bytes: a lane has column n of `rows` rows (0: none) from
+// row m, so that a warp's store is a piece of one row.  With eight columns a lane, one at a time, it was 32
+// pieces of eight rows: 780 rows by 912 -> 1470 18 us, 10 us so (9 us at 1472).  d: where the output starts.
+template <bool kGated>
+__device__ __forceinline__ void finish_column(const Epi &g, size_t d, int m, int n, int rows, float (&z)[32], float (&up)[32])
+{
+    if (rows <= 0)
+        return;
+    if (g.bias) {
+        const float b = g.bias[n], bu = kGated ? g.bias[g.n_cols + n] : 0.f;
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+            z[x] += b;
+            if (kGated)
+                up[x] += bu;
+        }
+    }
+    if (g.preact) {
+        const size_t off = (size_t)m * g.N + n;
+        if (g.type == kTypeF16) {
+            put_column<__half>(g.preact, off, g.N, rows, z);
+            if (kGated)
+                put_column<__half>(g.preact, off + g.n_cols, g.N, rows, up);
+        } else {
+            put_column<__nv_bfloat16>(g.preact, off, g.N, rows, z);
+            if (kGated)
+                put_column<__nv_bfloat16>(g.preact, off + g.n_cols, g.N, rows, up);
+        }
+    }
+    if (kGated) {
+#pragma unroll
+        for (int x = 0; x < 32; ++x)
+            z[x] *= sigmoid(z[x]) * up[x];
+    } else if (g.act == kActSilu) {
+#pragma unroll
+        for (int x = 0; x < 32; ++x)
+            z[x] = act_fwd(z[x], kActSilu);
+    } else if (g.act == kActGelu) {
+#pragma unroll
+        for (int x = 0; x < 32; ++x)
+            z[x] = act_fwd(z[x], kActGelu);
+    }
+    const size_t off = d + (size_t)m * g.n_cols + n;
+    if (g.out_type == kTypeF32)
+        end_column<float>(g, off, rows, z);
+    else if (g.out_type == kTypeF16)
+        end_column<__half>(g, off, rows, z);
+    else
+        end_column<__nv_bfloat16>(g, off, rows, z);
 }
 
 // Bias and activation of 64 columns of one row from column n.
@@ -726,6 +804,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         };
+        // 32 columns of this warp's 32 rows (lane: row) to lane: column
+        auto turn_columns = [&](const uint32_t (&r)[32], float (&v)[32]) {
+            float4 *own = reinterpret_cast<float4 *>(stg + lane * 32);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                own[j ^ (lane & 7)] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                                  __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+                v[x] = stg[x * 32 + (((lane >> 2) ^ (x & 7)) << 2) + (lane & 3)];
+            __syncwarp();
+        };
         // Accumulator n of this pair is complete; `free_acc` gives its TMEM back to the MMAs.
         auto wait_acc = [&]() {
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(acc_full(n & 1), (n >> 1) & 1, &g_linear_err, kWaitNs));
@@ -786,7 +877,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     else
                         ahead.load(ep, w);
                 };
-                auto done = [&](const uint32_t (&r)[32]) {
+                auto done = [&](int c, const uint32_t (&r)[32]) {
+                    if (!ep.vec) { // a lane has a column of 32 tokens as it is
+                        const int m = t.row + c * 32;
+                        const int col = gated ? t.n0 + (int)rank * 64 + q * 16 + (lane & 15)
+                                              : t.n0 + (int)rank * 128 + q * 32 + lane;
+                        const int rows = col < g.n_cols ? min(32, t.row_end - m) : 0;
+                        float v[32], up[32];
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            v[x] = __uint_as_float(r[x]);
+                        if (gated) { // the up half lies 16 lanes on
+#pragma unroll
+                            for (int x = 0; x < 32; ++x)
+                                up[x] = __shfl_down_sync(0xFFFFFFFFu, v[x], 16);
+                            finish_column<true>(ep, d_off, m, col, lane < 16 ? rows : 0, v, up);
+                        } else {
+                            finish_column<false>(ep, d_off, m, col, rows, v, v);
+                        }
+                        return;
+                    }
                     put(r);
                     if (gated) {
                         float v[2][8], up[2][8];
@@ -835,7 +945,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < 2; ++c)
                         if (half + 2 * c < chunks) {
                             place(half + 2 * c);
-                            done(sum[c]);
+                            done(half + 2 * c, sum[c]);
                         }
                 } else {
                     if (half < chunks)
@@ -852,7 +962,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tmem_wait_ld();
                         if (c + 2 >= chunks)
                             free_acc();
-                        done(r);
+                        done(c, r);
                     }
                 }
                 continue;
@@ -872,6 +982,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ahead.load(ep, w);
             };
             const uint32_t lanes = (uint32_t)(q * 32) << 16;
+            // rows without 16-byte starts: this warp's rows of column c + lane of the tile
+            const int row32 = row0 - rl;
+            auto column_rows = [&](int c) { return t.n0 + c + lane < g.n_cols ? min(32, t.row_end - row32) : 0; };
             if constexpr (kSum) {
                 // columns lc .. of D (gated: and the same of the up half) summed over the chains
                 constexpr int kChunks = BN / 64;
@@ -912,6 +1025,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < kChunks / 2; ++c) {
                             float v[4][8], up[4][8];
                             const int lc = half * cols + c * 32;
+                            if (!ep.vec) {
+                                float z[32], u[32];
+                                turn_columns(sum[c], z);
+                                turn_columns(sum[c + kChunks / 2], u);
+                                finish_column<true>(ep, d_off, row32, t.n0 + lc + lane, column_rows(lc), z, u);
+                                continue;
+                            }
                             place(lc);
                             turn(sum[c], v);
                             turn(sum[c + kChunks / 2], up);
@@ -923,6 +1043,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < kChunks; ++c) {
                         float v[4][8], up[4][8];
                         const int lc = half * cols + c * 32;
+                        if (!ep.vec) {
+                            float z[32];
+                            turn_columns(sum[c], z);
+                            finish_column<false>(ep, d_off, row32, t.n0 + lc + lane, column_rows(lc), z, z);
+                            continue;
+                        }
                         place(lc);
                         turn(sum[c], v);
                         finish<4, false>(ep, w, v, up, ahead);
@@ -992,8 +1118,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_wait_ld();
                     turn(r, f);
                 };
+                auto take_columns = [&](uint32_t col, float (&f)[32]) {
+                    uint32_t r[32];
+                    tmem_ld32(tmem + 256u * (n & 1) + lanes + col, r);
+                    tmem_wait_ld();
+                    turn_columns(r, f);
+                };
                 for (int c = 0; c < cols; c += 32) {
                     const int lc = half * cols + c; // column within the tile
+                    if (!ep.vec) {
+                        if (c == 0 && t.nkb > 0 && !wait_acc())
+                            break;
+                        float z[32] = {}, u[32] = {};
+                        const bool gated = !kPlain && g.gated;
+                        if (t.nkb > 0) {
+                            take_columns(lc, z);
+                            if (gated)
+                                take_columns(BN / 2 + lc, u);
+                            if (c + 32 >= cols)
+                                free_acc();
+                        }
+                        if (gated)
+                            finish_column<true>(ep, d_off, row32, t.n0 + lc + lane, column_rows(lc), z, u);
+                        else
+                            finish_column<false>(ep, d_off, row32, t.n0 + lc + lane, column_rows(lc), z, u);
+                        continue;
+                    }
                     place(lc);
                     if (c == 0 && t.nkb > 0 && !wait_acc())
                         break;
