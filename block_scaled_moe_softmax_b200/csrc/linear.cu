@@ -1243,46 +1243,54 @@ struct PackArgs {
     Segments seg;           // of x's rows: padding is left out
 };
 
-// One CTA per row (grid y: x or w); a thread copies 8 elements, two at a time from aligned words that its
-// row may start in the middle of.
+constexpr int kPackCols = 1024; // of a warp: a lane has four chunks of 8 in flight
+
+// A warp per piece of a row (grid y: x or w); a lane copies 8 elements at a time from aligned words that its
+// row may start in the middle of.  Latency bounds it: 780 + 1470 rows of 909 4.2 us, 9.7 us with a CTA a row
+// and a chunk at a time.
 __global__ void __launch_bounds__(256) pack_kernel(const PackArgs a)
 {
     grid_dep_wait();
     grid_dep_launch();
-    const int o = a.src[0] ? blockIdx.y : 1;
-    for (int64_t r = blockIdx.x; r < a.rows[o]; r += gridDim.x) {
+    const int o = a.src[0] ? blockIdx.y : 1, lane = threadIdx.x & 31;
+    const int pieces = (a.cols + kPackCols - 1) / kPackCols;
+    const int64_t items = a.rows[o] * pieces;
+    for (int64_t i = blockIdx.x * 8 + (threadIdx.x >> 5); i < items; i += gridDim.x * 8) {
+        const int64_t r = i / pieces;
         int e;
         int64_t end;
         if (o == 0 && a.seg.E && !find_segment(a.seg, r, e, end))
             continue;
+        const int first = (int)(i % pieces) * kPackCols, last = min(a.cols, first + kPackCols);
         const uint16_t *src = a.src[o] + r * a.cols;
         uint16_t *dst = a.dst[o] + r * a.ld;
         const bool odd = reinterpret_cast<uintptr_t>(src) & 2;
-        for (int c = threadIdx.x * 8; c < a.cols; c += 256 * 8) {
-            if (c + 8 > a.cols) {
-                for (int i = c; i < a.cols; ++i)
-                    dst[i] = src[i];
-                continue;
-            }
-            uint32_t v[4];
-            if (odd) { // the words around the eight: the first holds the element before them, which is
-                       // in the buffer (an odd row is not the first), and the last ends with the eighth
-                const uint32_t *p = reinterpret_cast<const uint32_t *>(src + c - 1);
-                uint32_t lo = p[0];
+        uint32_t v[4][5];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t hi = i < 3 ? p[i + 1] : src[c + 7];
-                    v[i] = __funnelshift_r(lo, hi, 16);
-                    lo = hi;
-                }
-            } else {
-                const uint32_t *p = reinterpret_cast<const uint32_t *>(src + c);
+        for (int j = 0; j < 4; ++j) {
+            // odd: the words around the eight.  The first holds the element before them, which is in the
+            // buffer (an odd row is not the first), and the last ends with the eighth
+            const int c = first + lane * 8 + j * 256;
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(src + c - (odd ? 1 : 0));
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[i] = p[i];
-            }
-            *reinterpret_cast<uint4 *>(dst + c) = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int x = 0; x < 4; ++x)
+                v[j][x] = c + 8 <= last ? p[x] : 0u;
+            v[j][4] = odd && c + 8 <= last ? src[c + 7] : 0u;
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = first + lane * 8 + j * 256;
+            if (c + 8 > last)
+                continue;
+            if (odd)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    v[j][x] = __funnelshift_r(v[j][x], v[j][x + 1], 16);
+            *reinterpret_cast<uint4 *>(dst + c) = make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
+        }
+        const int rest = (last & ~7) + lane; // pieces start at multiples of 8
+        if (rest < last)
+            dst[rest] = src[rest];
     }
 }
 
@@ -1298,7 +1306,8 @@ cudaError_t launch_pack(const void *&x, int64_t x_rows, const Segments &seg, cha
     a.rows[0] = x_rows, a.rows[1] = w_rows;
     a.cols = K, a.ld = (int)round_up(K, 8), a.seg = seg;
     const int64_t most = !x ? w_rows : !w ? x_rows : x_rows > w_rows ? x_rows : w_rows;
-    const dim3 grid((unsigned)(most < 148 * 8 ? most : 148 * 8), x && w ? 2 : 1);
+    const int64_t ctas = (most * ((K + kPackCols - 1) / kPackCols) + 7) / 8;
+    const dim3 grid((unsigned)(ctas < 148 * 8 ? ctas : 148 * 8), x && w ? 2 : 1);
     if (x)
         x = x_ws;
     if (w)
