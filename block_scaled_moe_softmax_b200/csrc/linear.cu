@@ -236,86 +236,51 @@ struct Rows {
     __device__ __forceinline__ size_t at(int j) const { return o + (size_t)j * so; }
 };
 
-// Residual values of R rows x 8 columns, loaded ahead of their use (aligned rows only).
+// Residual values (16-bit) of R rows x 8 columns, loaded ahead of their use.
 template <int R> struct Ahead {
-    uint4 a[R], b[R];
+    uint4 a[R];
     __device__ __forceinline__ void load(const Epi &g, const Rows &w)
     {
-        if (!g.residual || !g.vec)
+        if (!g.residual)
             return;
-        if (g.out_type == kTypeF32) {
-            const float *p = static_cast<const float *>(g.residual);
-#pragma unroll
-            for (int j = 0; j < R; ++j)
-                if (w.has(j)) {
-                    a[j] = reinterpret_cast<const uint4 *>(p + w.at(j))[0];
-                    b[j] = reinterpret_cast<const uint4 *>(p + w.at(j))[1];
-                }
-        } else {
-            const uint16_t *p = static_cast<const uint16_t *>(g.residual);
-#pragma unroll
-            for (int j = 0; j < R; ++j)
-                if (w.has(j))
-                    a[j] = *reinterpret_cast<const uint4 *>(p + w.at(j));
-        }
-    }
-};
-
-template <typename T, int R>
-__device__ __forceinline__ void add_rows(const Epi &g, const Ahead<R> &ahead, const Rows &w, float (&v)[R][8])
-{
-    if (R > 1 || g.vec) { // finish_column has the tiles' others
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            Raw<T, 8> r;
-            float f[8];
-            if constexpr (sizeof(T) == 4) {
-                r.a = *reinterpret_cast<const float4 *>(&ahead.a[j]);
-                r.b = *reinterpret_cast<const float4 *>(&ahead.b[j]);
-            } else {
-                r.v = ahead.a[j];
-            }
-            r.get(f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) // rows not stored hold what they hold
-                v[j][i] += f[i];
-        }
-        return;
-    }
-    const T *p = static_cast<const T *>(g.residual);
-#pragma unroll
-    for (int j = 0; j < R; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (w.has(j) && w.n + i < g.n_cols)
-                v[j][i] += to_f32<T>(p[w.at(j) + i]);
-}
-
-template <typename T, int R>
-__device__ __forceinline__ void put_rows(T *p, int step, const Epi &g, const Rows &w, const float (&v)[R][8])
-{
-    if (R > 1 || g.vec) {
+        const uint16_t *p = static_cast<const uint16_t *>(g.residual);
 #pragma unroll
         for (int j = 0; j < R; ++j)
             if (w.has(j))
-                Raw<T, 8>::put(p + (size_t)j * step, v[j]);
-        return;
+                a[j] = *reinterpret_cast<const uint4 *>(p + w.at(j));
     }
+};
+
+template <typename T, int R> __device__ __forceinline__ void add_rows(const Ahead<R> &ahead, float (&v)[R][8])
+{
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        Raw<T, 8> r;
+        float f[8];
+        r.v = ahead.a[j];
+        r.get(f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) // rows not stored hold what they hold
+            v[j][i] += f[i];
+    }
+}
+
+template <typename T, int R>
+__device__ __forceinline__ void put_rows(T *p, int step, const Rows &w, const float (&v)[R][8])
+{
 #pragma unroll
     for (int j = 0; j < R; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (w.has(j) && w.n + i < g.n_cols)
-                p[(size_t)j * step + i] = from_f32<T>(v[j][i]);
+        if (w.has(j))
+            Raw<T, 8>::put(p + (size_t)j * step, v[j]);
 }
 
 template <int R>
 __device__ __forceinline__ void put_preact(size_t off, const Epi &g, const Rows &w, const float (&v)[R][8])
 {
     if (g.type == kTypeF16)
-        put_rows<__half, R>(static_cast<__half *>(g.preact) + off, w.spo, g, w, v);
+        put_rows<__half, R>(static_cast<__half *>(g.preact) + off, w.spo, w, v);
     else
-        put_rows<__nv_bfloat16, R>(static_cast<__nv_bfloat16 *>(g.preact) + off, w.spo, g, w, v);
+        put_rows<__nv_bfloat16, R>(static_cast<__nv_bfloat16 *>(g.preact) + off, w.spo, w, v);
 }
 
 template <int R> __device__ __forceinline__ void add_bias(const float *b, const Epi &g, const Rows &w, float (&v)[R][8])
@@ -364,18 +329,14 @@ __device__ __forceinline__ void finish(const Epi &g, const Rows &w, float (&z)[R
             for (int i = 0; i < 8; ++i)
                 z[j][i] = act_fwd(z[j][i], kActGelu);
     }
-    if (g.out_type == kTypeF32) {
+    if (g.out_type == kTypeF16) {
         if (g.residual)
-            add_rows<float, R>(g, ahead, w, z);
-        put_rows<float, R>(static_cast<float *>(g.out) + w.o, w.so, g, w, z);
-    } else if (g.out_type == kTypeF16) {
-        if (g.residual)
-            add_rows<__half, R>(g, ahead, w, z);
-        put_rows<__half, R>(static_cast<__half *>(g.out) + w.o, w.so, g, w, z);
+            add_rows<__half, R>(ahead, z);
+        put_rows<__half, R>(static_cast<__half *>(g.out) + w.o, w.so, w, z);
     } else {
         if (g.residual)
-            add_rows<__nv_bfloat16, R>(g, ahead, w, z);
-        put_rows<__nv_bfloat16, R>(static_cast<__nv_bfloat16 *>(g.out) + w.o, w.so, g, w, z);
+            add_rows<__nv_bfloat16, R>(ahead, z);
+        put_rows<__nv_bfloat16, R>(static_cast<__nv_bfloat16 *>(g.out) + w.o, w.so, w, z);
     }
 }
 
@@ -393,9 +354,15 @@ template <typename T> __device__ __forceinline__ void add_column(const void *res
 {
     const T *p = static_cast<const T *>(res) + off;
 #pragma unroll
-    for (int x = 0; x < 32; ++x, p += step)
-        if (x < rows)
-            v[x] += to_f32<T>(*p);
+    for (int x = 0; x < 32; x += 16) { // sixteen loads at a time
+        T f[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i, p += step)
+            f[i] = x + i < rows ? *p : from_f32<T>(0.f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            v[x + i] += to_f32<T>(f[i]);
+    }
 }
 
 template <typename T>
@@ -406,9 +373,11 @@ __device__ __forceinline__ void end_column(const Epi &g, size_t off, int rows, f
     put_column<T>(g.out, off, g.n_cols, rows, v);
 }
 
-// The same for outputs whose rows do not start on 16 bytes: a lane has column n of `rows` rows (0: none) from
-// row m, so that a warp's store is a piece of one row.  With eight columns a lane, one at a time, it was 32
-// pieces of eight rows: 780 rows by 912 -> 1470 18 us, 10 us so (9 us at 1472).  d: where the output starts.
+// The same for float32 outputs and for those whose rows do not start on 16 bytes: a lane has column n of
+// `rows` rows (0: none) from row m, so that a warp's store is a piece of one row.  With eight columns a lane,
+// ragged ones were stored one at a time, 32 pieces of eight rows: 780 rows by 912 -> 1470 18 us, 10 us so (9 us
+// at 1472).  Aligned float32 rows, eight columns a lane in two 16-byte stores: 483 rows by 872 -> 384 11.3 us,
+// 9.8 us so.  d: where the output starts.
 template <bool kGated>
 __device__ __forceinline__ void finish_column(const Epi &g, size_t d, int m, int n, int rows, float (&z)[32], float (&up)[32])
 {
@@ -455,6 +424,34 @@ __device__ __forceinline__ void finish_column(const Epi &g, size_t d, int m, int
         end_column<__half>(g, off, rows, z);
     else
         end_column<__nv_bfloat16>(g, off, rows, z);
+}
+
+// The same for one value: row m, column n.
+template <typename T, bool kGated>
+__device__ __forceinline__ void finish_value(const Epi &e, size_t m, int n, float z, float up)
+{
+    if (e.bias) {
+        z += e.bias[n];
+        if (kGated)
+            up += e.bias[e.n_cols + n];
+    }
+    if (e.preact) {
+        T *p = static_cast<T *>(e.preact) + m * e.N + n;
+        *p = from_f32<T>(z);
+        if (kGated)
+            p[e.n_cols] = from_f32<T>(up);
+    }
+    float v = kGated ? z * sigmoid(z) * up : act_fwd(z, e.act);
+    const size_t o = m * e.n_cols + n;
+    if (e.out_type == kTypeF32) {
+        if (e.residual)
+            v += static_cast<const float *>(e.residual)[o];
+        static_cast<float *>(e.out)[o] = v;
+    } else {
+        if (e.residual)
+            v += to_f32<T>(static_cast<const T *>(e.residual)[o]);
+        static_cast<T *>(e.out)[o] = from_f32<T>(v);
+    }
 }
 
 // Bias and activation of 64 columns of one row from column n.
@@ -835,6 +832,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Epi ep = kPlain ? Epi{nullptr, nullptr, g.out, nullptr, kActNone, g.N, g.n_cols, g.type, g.out_type, g.vec}
                                 : Epi{g.bias ? g.bias + (size_t)t.e * g.N : nullptr, g.residual, g.out, g.preact, g.act,
                                       g.N, g.n_cols, g.type, g.out_type, g.vec};
+            const bool columns = kSum || !ep.vec || ep.out_type == kTypeF32; // kSum: of float32 outputs
             const size_t d_off = g.seg_k ? (size_t)t.e * g.d_expert : (size_t)t.split * g.M * g.n_cols;
             if constexpr (kSwap) {
                 // lane: a column of D; chunk c: tokens 32 c .. + 31, taken by the warp halves in turn
@@ -878,7 +876,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         ahead.load(ep, w);
                 };
                 auto done = [&](int c, const uint32_t (&r)[32]) {
-                    if (!ep.vec) { // a lane has a column of 32 tokens as it is
+                    if (columns) { // a lane has a column of 32 tokens as it is
                         const int m = t.row + c * 32;
                         const int col = gated ? t.n0 + (int)rank * 64 + q * 16 + (lane & 15)
                                               : t.n0 + (int)rank * 128 + q * 32 + lane;
@@ -943,19 +941,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         break;
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
-                        if (half + 2 * c < chunks) {
-                            place(half + 2 * c);
+                        if (half + 2 * c < chunks)
                             done(half + 2 * c, sum[c]);
-                        }
                 } else {
-                    if (half < chunks)
+                    if (half < chunks && !columns)
                         place(half);
                     if (!wait_acc())
                         break;
                     if (half >= chunks)
                         free_acc();
                     for (int c = half; c < chunks; c += 2) {
-                        if (c > half)
+                        if (c > half && !columns)
                             place(c);
                         uint32_t r[32];
                         tmem_ld32(tmem + 256u * (n & 1) + acc0 + c * 32, r);
@@ -982,7 +978,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ahead.load(ep, w);
             };
             const uint32_t lanes = (uint32_t)(q * 32) << 16;
-            // rows without 16-byte starts: this warp's rows of column c + lane of the tile
+            // `columns`: this warp's rows of column c + lane of the tile
             const int row32 = row0 - rl;
             auto column_rows = [&](int c) { return t.n0 + c + lane < g.n_cols ? min(32, t.row_end - row32) : 0; };
             if constexpr (kSum) {
@@ -1023,39 +1019,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if constexpr (kChunks % 2 == 0) {
 #pragma unroll
                         for (int c = 0; c < kChunks / 2; ++c) {
-                            float v[4][8], up[4][8];
+                            float z[32], up[32];
                             const int lc = half * cols + c * 32;
-                            if (!ep.vec) {
-                                float z[32], u[32];
-                                turn_columns(sum[c], z);
-                                turn_columns(sum[c + kChunks / 2], u);
-                                finish_column<true>(ep, d_off, row32, t.n0 + lc + lane, column_rows(lc), z, u);
-                                continue;
-                            }
-                            place(lc);
-                            turn(sum[c], v);
-                            turn(sum[c + kChunks / 2], up);
-                            finish<4, true>(ep, w, v, up, ahead);
+                            turn_columns(sum[c], z);
+                            turn_columns(sum[c + kChunks / 2], up);
+                            finish_column<true>(ep, d_off, row32, t.n0 + lc + lane, column_rows(lc), z, up);
                         }
                     }
                 } else {
 #pragma unroll
                     for (int c = 0; c < kChunks; ++c) {
-                        float v[4][8], up[4][8];
+                        float z[32];
                         const int lc = half * cols + c * 32;
-                        if (!ep.vec) {
-                            float z[32];
-                            turn_columns(sum[c], z);
-                            finish_column<false>(ep, d_off, row32, t.n0 + lc + lane, column_rows(lc), z, z);
-                            continue;
-                        }
-                        place(lc);
-                        turn(sum[c], v);
-                        finish<4, false>(ep, w, v, up, ahead);
+                        turn_columns(sum[c], z);
+                        finish_column<false>(ep, d_off, row32, t.n0 + lc + lane, column_rows(lc), z, z);
                     }
                 }
             } else {
-                if (ep.vec && ep.out_type != kTypeF32 && cols % 64 == 0 && !ep.residual && !ep.preact &&
+                if (!columns && cols % 64 == 0 && !ep.residual && !ep.preact &&
                     (kPlain || !g.gated)) {
                     // One 16-bit output: bias, activation and rounding where the values lie (lane: row), turned
                     // 64 columns at a time as 16-bit values, stored as whole 128-byte lines.  Half the
@@ -1126,7 +1107,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 };
                 for (int c = 0; c < cols; c += 32) {
                     const int lc = half * cols + c; // column within the tile
-                    if (!ep.vec) {
+                    if (columns) {
                         if (c == 0 && t.nkb > 0 && !wait_acc())
                             break;
                         float z[32] = {}, u[32] = {};
@@ -1178,58 +1159,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- split products
-__device__ __forceinline__ void load_f32x8(const float *p, float (&f)[8])
-{
-    Raw<float, 8> r;
-    r.load(p);
-    r.get(f);
-}
-
-// out = epilogue(sum over the splits' float32 planes, in order); one thread per 8 columns of a row.
+// out = epilogue(sum over the splits' float32 planes, in order); one thread per value, eight loads at a time.
+// Latency bounds it: 100 rows by 7168 -> 384, 23 planes, 15 us with the product, 18 us with eight columns a thread;
+// -> 387, whose columns were loaded one by one there, 11 us and 21 us.
+template <typename T, bool kGated>
 __global__ void __launch_bounds__(256) reduce_kernel(const float *planes, int splits, int M, Epi g)
 {
     grid_dep_wait();
     grid_dep_launch();
-    const int per_row = (g.n_cols + 7) / 8;
-    const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-    if (i >= (int64_t)M * per_row)
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x; // a split product has fewer tiles than there are pairs
+    const uint32_t m = i / (uint32_t)g.n_cols, n = i % (uint32_t)g.n_cols;
+    if (m >= (uint32_t)M)
         return;
-    const int64_t m = i / per_row;
-    const int n = (int)(i % per_row) * 8;
-    const bool gated = g.act == kActSwiglu;
     const size_t plane = (size_t)M * g.N;
-    float z[1][8] = {}, up[1][8] = {};
-    const Rows w{(size_t)m * g.n_cols + n, (size_t)m * g.N + n, 0, 0, n, 1u};
-    Ahead<1> ahead;
-    ahead.load(g, w);
-    for (int s = 0; s < splits; ++s) {
-        const float *p = planes + s * plane + m * g.N + n;
-        if (g.vec) {
-            float f[8];
-            load_f32x8(p, f);
+    const float *p = planes + (size_t)m * g.N + n;
+    float z = 0.f, up = 0.f;
+    for (int s = 0; s < splits; s += 8) {
+        float a[8], b[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                z[0][j] += f[j];
-            if (gated) {
-                load_f32x8(p + g.n_cols, f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    up[0][j] += f[j];
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (n + j < g.n_cols) {
-                    z[0][j] += p[j];
-                    if (gated)
-                        up[0][j] += p[j + g.n_cols];
-                }
+        for (int j = 0; j < 8; ++j, p += plane) {
+            a[j] = s + j < splits ? p[0] : 0.f;
+            b[j] = kGated && s + j < splits ? p[g.n_cols] : 0.f;
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            z += a[j], up += b[j];
     }
-    if (gated)
-        finish<1, true>(g, w, z, up, ahead);
-    else
-        finish<1, false>(g, w, z, up, ahead);
+    finish_value<T, kGated>(g, m, (int)n, z, up);
 }
 
 // ---------------------------------------------------------------- unaligned rows
@@ -1499,28 +1455,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(const SmallArgs
                 if (kGated)
                     up += load_rank(&total[(16 + c) * (kNb * 8) + m], q);
             }
-            if (e.bias) {
-                z += e.bias[n];
-                if (kGated)
-                    up += e.bias[cols + n];
-            }
-            if (e.preact) {
-                T *p = static_cast<T *>(e.preact) + (size_t)m * e.N + n;
-                *p = from_f32<T>(z);
-                if (kGated)
-                    p[cols] = from_f32<T>(up);
-            }
-            float v = kGated ? z * sigmoid(z) * up : act_fwd(z, e.act);
-            const size_t o = (size_t)m * cols + n;
-            if (e.out_type == kTypeF32) {
-                if (e.residual)
-                    v += static_cast<const float *>(e.residual)[o];
-                static_cast<float *>(e.out)[o] = v;
-            } else {
-                if (e.residual)
-                    v += to_f32<T>(static_cast<const T *>(e.residual)[o]);
-                static_cast<T *>(e.out)[o] = from_f32<T>(v);
-            }
+            finish_value<T, kGated>(e, m, n, z, up);
         }
     }
     if (ranks > 1)
@@ -1914,9 +1849,12 @@ BackwardPlan plan_backward(int E, int64_t M, int N, int K, int act, int type, in
 // The sum of a split product's planes, through the epilogue.
 int launch_reduce(const float *planes, int splits, int64_t M, const Epi &e, cudaStream_t s)
 {
-    const int64_t n = M * ((e.n_cols + 7) / 8);
-    const cudaError_t ce = launch_kernel(reduce_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, true, planes,
-                                         splits, (int)M, e);
+    cudaError_t ce = cudaSuccess;
+    by_half(e.type, [&](auto zero) {
+        using T = decltype(zero);
+        auto kernel = e.act == kActSwiglu ? reduce_kernel<T, true> : reduce_kernel<T, false>;
+        ce = launch_kernel(kernel, dim3((unsigned)((M * e.n_cols + 255) / 256)), dim3(256), 0, s, true, planes, splits, (int)M, e);
+    });
     return ce == cudaSuccess ? MOE_MX_OK : cuda_fail(ce, "split sum launch");
 }
 
