@@ -1470,12 +1470,13 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(const SmallArgs
 // - Up to 16 rows: less than 48 M weights.  Larger ones stream faster through the tile product with 32 tokens a
 //   tile: 16 rows by 4096 -> 14336 (59 M) 35 us here and 25 us there, 8 rows by 4096 -> 8192 (34 M) 14 us
 //   here and 17 us there.
-// - Up to 64 rows (32 with SwiGLU, whose partial sums take twice the shared memory): less than 192 M
-//   multiplications, since every CTA reads its slice of all rows of x.  7168 -> 384: 17 rows 7.2 us here, 12.0 as
-//   split tiles, 64 rows 10.8 and 12.7; 64 rows by 4096 -> 1400 15.6 us here, 10.3 as tiles.
+// - Up to 64 rows (32 with SwiGLU, whose partial sums take twice the shared memory): x below 128 K elements and
+//   less than 192 M multiplications, since every CTA reads its slice of all rows of x.  17 rows by 7168 -> 384
+//   7.2 us here, 8.2 as split tiles, 32 rows 8.5 and 7.7, 64 rows 10.8 and 8.3; 24 rows by 2048 -> 512 5.0 and
+//   6.5; 64 rows by 2048 -> 1024 8.0 and 7.4.
 bool is_small(int64_t M, int64_t N, int K, bool gated)
 {
-    return K % 8 == 0 && (M <= 16 ? N * K < 48000000 : M <= (gated ? 32 : 64) && M * N * K < 192000000);
+    return K % 8 == 0 && (M <= 16 ? N * K < 48000000 : M <= (gated ? 32 : 64) && M * K < 128000 && M * N * K < 192000000);
 }
 
 int launch_small(const SmallArgs &args, int type, cudaStream_t s)
