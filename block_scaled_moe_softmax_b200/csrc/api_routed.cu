@@ -107,6 +107,17 @@ int check_workspace(void *ws, int64_t given, int64_t need, int dev)
     return check_ptr(ws, dev, "workspace");
 }
 
+int check_device(int device)
+{
+    int ndev = 0;
+    const cudaError_t ce = cudaGetDeviceCount(&ndev);
+    if (ce != cudaSuccess)
+        return cuda_fail(ce, "cudaGetDeviceCount");
+    if (device < 0 || device >= ndev)
+        return fail(MOE_MX_ERR_INVALID_ARG, "device %d out of range (%d devices)", device, ndev);
+    return MOE_MX_OK;
+}
+
 } // namespace
 
 extern "C" {
@@ -254,14 +265,23 @@ int moe_mx_linear(const void *x, const void *w, const float *bias, const void *r
 int moe_mx_linear_status(int device, void *stream)
 {
     clear_error();
-    int ndev = 0;
-    const cudaError_t ce = cudaGetDeviceCount(&ndev);
-    if (ce != cudaSuccess)
-        return cuda_fail(ce, "cudaGetDeviceCount");
-    if (device < 0 || device >= ndev)
-        return fail(MOE_MX_ERR_INVALID_ARG, "device %d out of range (%d devices)", device, ndev);
+    if (int rc = check_device(device))
+        return rc;
     const DeviceGuard guard(device);
     return linear_status(static_cast<cudaStream_t>(stream));
+}
+
+int moe_mx_debug_linear_watchdog(int device, int timeout_us, void *stream)
+{
+    clear_error();
+    if (timeout_us < 1 || timeout_us > 10000000)
+        return fail(MOE_MX_ERR_INVALID_ARG, "timeout_us=%d must be in [1, 1e7]", timeout_us);
+    if (int rc = check_device(device))
+        return rc;
+    const DeviceGuard guard(device);
+    if (int rc = linear_watchdog((unsigned long long)timeout_us * 1000ull, static_cast<cudaStream_t>(stream)))
+        return rc;
+    return launched("watchdog launch");
 }
 
 int moe_mx_linear_backward(const void *dout, const void *x, const void *w, const void *preact, const int32_t *counts,

@@ -485,7 +485,17 @@ __device__ __forceinline__ void bias_act(const Epi &g, int n, uint32_t (&r0)[32]
 // the sum in registers; a 2-byte output's own rounding is far larger.
 constexpr int kChain = 8;
 
-__device__ uint32_t g_linear_err; // set by a wait that gave up
+// Recorded by a wait that gave up, until linear_status reads it.  No wait looks at it: a product that failed
+// must not cut short the waits of a later call, or of one on another stream.
+__device__ uint32_t g_linear_err;
+
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity)
+{
+    if (mbar_wait_bounded(bar, parity, nullptr, kWaitNs))
+        return true;
+    atomicOr(&g_linear_err, kErrTimeout);
+    return false;
+}
 
 // kSwap: token rows in boxes of 16, 32 and 64 rows.  dw of grouped rows: each expert's last k block of
 // A and of B with zeros behind its rows, 64 rows an expert (after_kernel).
@@ -567,7 +577,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             return some;
         }
         const uint32_t r = c % kRing;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(tile_full(r), (c / kRing) & 1, &g_linear_err, kWaitNs)))
+        if (!__all_sync(0xFFFFFFFFu, wait_phase(tile_full(r), (c / kRing) & 1)))
             return false;
         const int4 x = ring[r * 3], y = ring[r * 3 + 1], z = ring[r * 3 + 2];
         __syncwarp();
@@ -644,8 +654,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 uint32_t s1 = s0 + 1, p1 = p0;
                 if (s1 == S)
                     s1 = 0, p1 ^= 1;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty(s0), p0, &g_linear_err, kWaitNs) &&
-                                                 (!two || mbar_wait_bounded(empty(s1), p1, &g_linear_err, kWaitNs)))) {
+                if (!__all_sync(0xFFFFFFFFu, wait_phase(empty(s0), p0) && (!two || wait_phase(empty(s1), p1)))) {
                     ok = false;
                     break;
                 }
@@ -712,7 +721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = pair; more; i += pairs, ++c) {
             more = early && c == 0 ? some : get_tile<BN, kSwap, kMostTok>(g, prefix, i, t);
             const uint32_t r = c % kRing;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(tile_empty(r), ((c / kRing) & 1) ^ 1, &g_linear_err, kWaitNs)))
+            if (!__all_sync(0xFFFFFFFFu, wait_phase(tile_empty(r), ((c / kRing) & 1) ^ 1)))
                 break;
             if (lane == 0) {
                 ring[r * 3] = make_int4(t.e, t.row, t.row_end, t.n0);
@@ -731,7 +740,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t idesc = idesc_f16(g.fmt, kAMn, kBMn, kTileM, kSwap ? t.tok : BN);
             for (int kb = 0; ok && kb < t.nkb;) {
                 const int buf = n & 1;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(acc_empty(buf), ((n >> 1) & 1) ^ 1, &g_linear_err, kWaitNs))) {
+                if (!__all_sync(0xFFFFFFFFu, wait_phase(acc_empty(buf), ((n >> 1) & 1) ^ 1))) {
                     ok = false;
                     break;
                 }
@@ -745,7 +754,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int s = 0; s < S; ++s) {
                         if (s != (int)stage || kb >= end)
                             continue;
-                        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(full(s), phase, &g_linear_err, kWaitNs))) {
+                        if (!__all_sync(0xFFFFFFFFu, wait_phase(full(s), phase))) {
                             ok = false;
                             break;
                         }
@@ -816,7 +825,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         // Accumulator n of this pair is complete; `free_acc` gives its TMEM back to the MMAs.
         auto wait_acc = [&]() {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(acc_full(n & 1), (n >> 1) & 1, &g_linear_err, kWaitNs));
+            ok = __all_sync(0xFFFFFFFFu, wait_phase(acc_full(n & 1), (n >> 1) & 1));
             tc_fence_after();
             return ok;
         };
@@ -2042,6 +2051,16 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
         if (g.splits > 1)
             return launch_reduce(reinterpret_cast<float *>(ws + f.planes), g.splits, a.N, ep, s);
     }
+    return MOE_MX_OK;
+}
+
+int linear_watchdog(unsigned long long timeout_ns, cudaStream_t s)
+{
+    void *word = nullptr;
+    const cudaError_t ce = cudaGetSymbolAddress(&word, g_linear_err);
+    if (ce != cudaSuccess)
+        return cuda_fail(ce, "cudaGetSymbolAddress(error word)");
+    launch_watchdog(static_cast<uint32_t *>(word), timeout_ns, s);
     return MOE_MX_OK;
 }
 

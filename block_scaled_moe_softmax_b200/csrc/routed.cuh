@@ -63,5 +63,7 @@ int launch_linear(const LinearArgs &a, cudaStream_t s);
 int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s);
 // Synchronises s; MOE_MX_ERR_TIMEOUT if a wait of the current device's products gave up.
 int linear_status(cudaStream_t s);
+// One kernel whose wait runs out after timeout_ns, recorded as a product's would be.
+int linear_watchdog(unsigned long long timeout_ns, cudaStream_t s);
 
 } // namespace moe_mx

@@ -80,6 +80,7 @@ SIGNATURES = {
     "moe_mx_linear_backward": (_I, [_P] * 6 + [_I, _I64] + [_I] * 5 + [_P, _P, _P, _P, _I64, _P]),
     "moe_mx_linear_backward_workspace": (_I64, [_I, _I64] + [_I] * 5),
     "moe_mx_linear_status": (_I, [_I, _P]),
+    "moe_mx_debug_linear_watchdog": (_I, [_I, _I, _P]),
 }
 STAGES = ("route", "gather", "fc1", "fc2", "combine")
 
@@ -309,6 +310,10 @@ def moe_mx_linear_backward(dout, x, w, preact, counts, pad_offsets, num_experts:
 def moe_mx_linear_status(device: int, stream=None) -> int:
     """Returns the status code (does not raise on MOE_MX_ERR_TIMEOUT)."""
     return load_library().moe_mx_linear_status(device, _stream(stream))
+
+
+def moe_mx_debug_linear_watchdog(device: int, timeout_us: int, stream=None) -> None:
+    _check(load_library().moe_mx_debug_linear_watchdog(device, timeout_us, _stream(stream)))
 
 
 # ------------------------------------------------------------------ convenience wrappers

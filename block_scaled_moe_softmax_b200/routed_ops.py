@@ -18,6 +18,11 @@ stream of the tensors' device) and allocates only what it returns and its worksp
 allocator, as under ``with torch.cuda.stream(stream)``.  Wrong types, shapes or
 devices raise TypeError or ValueError before anything is enqueued.  Output buffers may be passed in
 (``out``, ``dy``, ``dx``); rows of grouped buffers that hold no pair (padding) are never written.
+
+Every wait inside linear and linear_backward is bounded.  Calls return before their kernels run, so one whose
+wait gives up (a GPU that stalls for seconds) leaves its result unfinished without an error there:
+``check()`` waits for a stream and raises if that happened.  Call it where results leave the GPU anyway,
+e.g. once a step.
 """
 from __future__ import annotations
 
@@ -313,3 +318,17 @@ def linear_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, preact
     _call("moe_mx_linear_backward", dout.data_ptr(), x.data_ptr(), w.data_ptr(), _ptr(preact), counts, pad, E, rows, N,
           K, dt, act, gt, _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), need, on)
     return dx, dw, db
+
+
+def check(device: torch.device | int | None = None, stream=None) -> None:
+    """Wait for ``stream`` (default: the device's current one) and raise MoeMxError (code MOE_MX_ERR_TIMEOUT) if
+    a linear or linear_backward of the device (default: the current one) left a result unfinished since the
+    last check.  Later calls are not affected by one that failed."""
+    dev = torch.device("cuda") if device is None else torch.device("cuda", device) if isinstance(device, int) else \
+        torch.device(device)
+    if dev.type != "cuda":
+        raise ValueError(f"device must be a CUDA device, not {dev}")
+    index = torch.cuda.current_device() if dev.index is None else dev.index
+    if stream is None:
+        stream = _raw_stream(index)
+    _call("moe_mx_linear_status", index, stream if isinstance(stream, int) else stream.cuda_stream)

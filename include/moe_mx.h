@@ -477,8 +477,8 @@ MOE_MX_API int moe_mx_route_group_noalloc(const float *router_logits, int num_to
  *   logits = linear(x, w_router)          -> moe_mx_route_group_noalloc
  *   grouped = dispatch(x)                 h = linear(grouped, w1[e], swiglu)
  *   y = linear(h, w2[e])                  out = combine(y, topk_w)
- * They need no handle, allocate nothing, keep nothing between calls, and may be captured in a CUDA
- * graph.  A call runs on the device that holds its first tensor; `stream` is a stream of that
+ * They need no handle, allocate nothing, keep nothing between calls that a later one uses, and may be
+ * captured in a CUDA graph.  A call runs on the device that holds its first tensor; `stream` is a stream of that
  * device.  Calls on different streams do not disturb one another as long as their output and
  * workspace buffers differ.  No atomics: equal inputs give equal bits.
  *
@@ -590,10 +590,19 @@ MOE_MX_API int64_t moe_mx_linear_backward_workspace(int num_experts, int64_t row
 
 /*
  * Synchronise `stream` and read the error word of `device`'s linear products: MOE_MX_OK,
- * MOE_MX_ERR_TIMEOUT if a bounded wait in one of them gave up since the last call (its results are then
- * incomplete; the word is cleared), or MOE_MX_ERR_CUDA.  Synchronous.  Errors: INVALID_ARG, CUDA.
+ * MOE_MX_ERR_TIMEOUT if a bounded wait (2 s) in one of them gave up since the last call (its results are
+ * then incomplete; the word is cleared), or MOE_MX_ERR_CUDA.  Synchronous.  The products are enqueued and
+ * return before they run, so this is where such a failure shows; the word only records it, and calls after
+ * a failed one, or beside it, are not affected.  Errors: INVALID_ARG, CUDA.
  */
 MOE_MX_API int moe_mx_linear_status(int device, void *stream);
+
+/*
+ * Self-test of that report: launch one kernel on `device` that waits on a device flag nothing sets, with
+ * a wait limit of timeout_us microseconds.  The wait gives up, the kernel records it in the word that
+ * moe_mx_linear_status reads and returns.  Nothing faults or traps.  Errors: INVALID_ARG, CUDA.
+ */
+MOE_MX_API int moe_mx_debug_linear_watchdog(int device, int timeout_us, void *stream);
 
 #ifdef __cplusplus
 }

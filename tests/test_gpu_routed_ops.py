@@ -647,3 +647,24 @@ def test_errors_on_the_device_are_refused():
     with pytest.raises(moe_mx.MoeMxError, match="workspace"):
         moe_mx.moe_mx_linear_backward(rnd((8, 16), F, 66), x, w, None, None, None, 0, 8, 16, 64, 0, 0, 1,
                                       torch.empty_like(x), None, None, None, 0)
+
+
+# ---------------------------------------------------------------- failure detection
+def test_a_wait_that_gives_up_is_reported_and_harms_no_other_call():
+    ops.check()
+    x, w = rnd((300, 131072), BF, 100), rnd((264, 131072), BF, 101, 2.0 ** -8)
+    want = ops.linear(x, w, activation="silu")  # waits of more than 100 us for its accumulators
+    moe_mx.moe_mx_debug_linear_watchdog(0, 2000)  # a 2 ms wait on a flag nothing sets
+    got = [ops.linear(x, w, activation="silu") for _ in range(3)]  # the word is set by now
+    with pytest.raises(moe_mx.MoeMxError) as e:
+        ops.check()
+    assert e.value.code == moe_mx.MOE_MX_ERR_TIMEOUT
+    for t in got:
+        assert torch.equal(t, want)
+    ops.check()  # read and cleared
+    s = torch.cuda.Stream()
+    moe_mx.moe_mx_debug_linear_watchdog(0, 2000, s)
+    with pytest.raises(moe_mx.MoeMxError):
+        ops.check("cuda:0", s)
+    ops.check(0, s.cuda_stream)
+    assert moe_mx.moe_mx_linear_status(0) == moe_mx.MOE_MX_OK

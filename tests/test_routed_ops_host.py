@@ -131,3 +131,11 @@ def test_grouped_rows_bound_is_the_librarys():
     for pairs, experts in ((0, 4), (1, 4), (8, 4), (500, 384)):
         hit = min(pairs, experts)
         assert ops.max_grouped_rows(pairs, experts) == -(-(pairs + hit * 127) // 128) * 128
+
+
+def test_watchdog_and_check_refuse(lib):
+    for us in (0, -1, 10000001):
+        assert lib.moe_mx_debug_linear_watchdog(0, us, None) == BAD and "timeout_us" in _err()
+    assert lib.moe_mx_debug_linear_watchdog(-1, 1000, None) in (BAD, moe_mx.MOE_MX_ERR_CUDA)
+    with pytest.raises(ValueError, match="CUDA device"):
+        ops.check("cpu")
