@@ -121,6 +121,7 @@ struct Gemm {
     int tok;              // kSwap, dense: tokens of a tile
     int gated;            // swiglu: gate and up rows in one tile (of B halves; kSwap: 16 by 16 rows of A)
     int fmt;              // 0: f16, 1: bf16
+    int run_log;          // log2 of the k blocks that one accumulator sums (!kSum)
     // epilogue
     const float *bias;
     const void *residual;
@@ -129,10 +130,14 @@ struct Gemm {
     int type, out_type, vec;
     int wide_a, wide_b;   // an M- or N-major operand of whole 64-element groups: one copy takes all of them
     int64_t d_expert;     // elements from one expert's D to the next's (seg_k)
+    float4 *held;         // sums of tiles of more than one run, kHeld of every epilogue warp (kHeldBytes in all)
 };
 
 constexpr int kTileM = 256, kBk = 64, kMaxSeg = kMaxExperts;
 constexpr int kThreads = 384, kEpiWarps = 8;
+constexpr int kPairs = 74; // SM pairs of the 148-SM part the plans are made for
+constexpr int kHeldChunk = 32 * 32 / 4, kHeld = 4 * kHeldChunk; // float4s of 32 x 32 values; of a warp's four
+constexpr int64_t kHeldBytes = (int64_t)kPairs * 2 * kEpiWarps * kHeld * 16;
 constexpr int kRing = 4, kTileInts = 12; // tiles decoded ahead, and the words of one
 constexpr unsigned long long kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
 
@@ -480,10 +485,15 @@ __device__ __forceinline__ void bias_act(const Epi &g, int n, uint32_t (&r0)[32]
 }
 
 // The tensor core adds into its float32 accumulator by truncation: a chain over K = 7168 is off by
-// 8e-6 in relative norm (measured), where a rounding sum is by 9e-7.  Products with float32 outputs
-// therefore hand the accumulator over every kChain k blocks (kSum) and the epilogue's warps keep
-// the sum in registers; a 2-byte output's own rounding is far larger.
+// 8e-6 in relative norm (measured), where a rounding sum is by 9e-7, and a sum of products of one sign by
+// 6.5e-9 of itself per k.  Products with float32 outputs therefore hand the accumulator over every kChain k
+// blocks (kSum) and the epilogue's warps keep the sum in registers.  Other products do so every 2^run_log
+// k blocks, where such a chain is off by a ninth of half a step of the output's type (8192 of k and 5.3e-5 for
+// float16, 65536 and 4.3e-4 for bf16), and keep the sum in the workspace (Gemm::held): dw sums over as many rows as
+// there are, and in one chain of 300,000 rows of one sign a float16 one was off by 2e-3.  A handover costs
+// about 9 us (4096 x 4096 weights' gradient over 65536 rows: 1510 us in one chain, 1570 in eight).
 constexpr int kChain = 8;
+inline int run_log(int type) { return type == kTypeF16 ? 7 : 10; }
 
 // Recorded by a wait that gave up, until linear_status reads it.  No wait looks at it: a product that failed
 // must not cut short the waits of a later call, or of one on another stream.
@@ -746,7 +756,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 ++n;
                 tc_fence_after();
-                const int first = kb, end = kSum ? min(t.nkb, kb + kChain) : t.nkb;
+                const int first = kb, end = min(t.nkb, kb + (kSum ? kChain : 1 << g.run_log));
                 while (ok && kb < end) {
                     // unrolled over the stages, whose descriptors are then constants apart (about 100 cycles less
                     // a block; descriptors are affine in the address, which stays below 2^18)
@@ -835,6 +845,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0)
                 mbar_arrive_relaxed(map_rank(acc_empty(n & 1), 0)); // its TMEM reads are done (wait::ld)
             ++n;
+        };
+        // The sums of a tile of more than one run (!kSum): those of all its runs but the last, 32 x 32 at a
+        // time from column `col(i)` of TMEM, i < chunks, go to this warp's part of the workspace, which
+        // `add_held` adds to the last run's.  A lane reads what it wrote.
+        float4 *const held = g.held + ((size_t)blockIdx.x * kEpiWarps + (warp - 4)) * kHeld + lane;
+        int runs = 0; // of this tile, before its last
+        auto add_held = [&](int i, uint32_t (&r)[32]) {
+            if (!runs)
+                return;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float4 h = held[i * kHeldChunk + j * 32];
+                r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + h.x);
+                r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + h.y);
+                r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + h.z);
+                r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + h.w);
+            }
+        };
+        auto hold_runs = [&](int nkb, int chunks, auto col) {
+            const int most = (nkb - 1) >> g.run_log;
+            for (runs = 0; runs < most; ++runs) {
+                if (!wait_acc())
+                    return false;
+                for (int i = 0; i < chunks; ++i) {
+                    uint32_t r[32];
+                    tmem_ld32(tmem + 256u * (n & 1) + ((uint32_t)(q * 32) << 16) + col(i), r);
+                    tmem_wait_ld();
+                    add_held(i, r); // of the runs before
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        held[i * kHeldChunk + j * 32] =
+                            make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                        __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+                }
+                free_acc();
+            }
+            return true;
         };
         while (ok && next(c)) {
             // gradients have no bias, preact, activation or residual
@@ -953,6 +1000,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (half + 2 * c < chunks)
                             done(half + 2 * c, sum[c]);
                 } else {
+                    if (!hold_runs(t.nkb, (chunks - half + 1) / 2, [&](int i) { return (half + 2 * i) * 32; }))
+                        break;
                     if (half < chunks && !columns)
                         place(half);
                     if (!wait_acc())
@@ -965,6 +1014,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         uint32_t r[32];
                         tmem_ld32(tmem + 256u * (n & 1) + acc0 + c * 32, r);
                         tmem_wait_ld();
+                        add_held(c / 2, r);
                         if (c + 2 >= chunks)
                             free_acc();
                         done(c, r);
@@ -1045,8 +1095,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             } else {
+                constexpr int kChunks = BN / 64; // gated: half of them of the up half
+                const bool gated = !kPlain && g.gated;
+                if (!hold_runs(t.nkb, kChunks, [&](int i) {
+                        return half * cols + (gated && i >= kChunks / 2 ? BN / 2 + (i - kChunks / 2) * 32 : i * 32);
+                    }))
+                    break;
                 if (!columns && cols % 64 == 0 && !ep.residual && !ep.preact &&
-                    (kPlain || !g.gated)) {
+                    !gated) {
                     // One 16-bit output: bias, activation and rounding where the values lie (lane: row), turned
                     // 64 columns at a time as 16-bit values, stored as whole 128-byte lines.  Half the
                     // shared-memory traffic of float32 blocks of 32 columns; it bounds products of short k, such
@@ -1063,6 +1119,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             tmem_ld32(tmem + 256u * (n & 1) + lanes + lc, r0);
                             tmem_ld32(tmem + 256u * (n & 1) + lanes + lc + 32, r1);
                             tmem_wait_ld();
+                            add_held(c / 32, r0);
+                            add_held(c / 32 + 1, r1);
                             if (c + 64 >= cols)
                                 free_acc();
                         }
@@ -1102,16 +1160,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     continue;
                 }
-                auto take = [&](uint32_t col, float (&f)[4][8]) {
+                auto take = [&](uint32_t col, int chunk, float (&f)[4][8]) {
                     uint32_t r[32];
                     tmem_ld32(tmem + 256u * (n & 1) + lanes + col, r);
                     tmem_wait_ld();
+                    add_held(chunk, r);
                     turn(r, f);
                 };
-                auto take_columns = [&](uint32_t col, float (&f)[32]) {
+                auto take_columns = [&](uint32_t col, int chunk, float (&f)[32]) {
                     uint32_t r[32];
                     tmem_ld32(tmem + 256u * (n & 1) + lanes + col, r);
                     tmem_wait_ld();
+                    add_held(chunk, r);
                     turn_columns(r, f);
                 };
                 for (int c = 0; c < cols; c += 32) {
@@ -1120,11 +1180,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (c == 0 && t.nkb > 0 && !wait_acc())
                             break;
                         float z[32] = {}, u[32] = {};
-                        const bool gated = !kPlain && g.gated;
                         if (t.nkb > 0) {
-                            take_columns(lc, z);
+                            take_columns(lc, c / 32, z);
                             if (gated)
-                                take_columns(BN / 2 + lc, u);
+                                take_columns(BN / 2 + lc, kChunks / 2 + c / 32, u);
                             if (c + 32 >= cols)
                                 free_acc();
                         }
@@ -1139,10 +1198,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         break;
                     float v[4][8] = {}, up[4][8] = {};
                     if (t.nkb > 0)
-                        take(lc, v);
-                    if (!kPlain && g.gated) {
+                        take(lc, c / 32, v);
+                    if (gated) {
                         if (t.nkb > 0) {
-                            take(BN / 2 + lc, up);
+                            take(BN / 2 + lc, kChunks / 2 + c / 32, up);
                             if (c + 32 >= cols)
                                 free_acc();
                         }
@@ -1281,8 +1340,6 @@ cudaError_t launch_pack(const void *&x, int64_t x_rows, const Segments &seg, cha
 }
 
 // ---------------------------------------------------------------- launch
-constexpr int kPairs = 74; // SM pairs of the 148-SM part the plans are made for
-
 // The shape of a dense [M, cols] product over kb blocks of k, by the estimated cycles: a 64-deep block of a
 // 256 x BN tile (BN weight rows, or BN tokens for kSwap) takes about 256 + BN cycles (its MMAs 2 BN,
 // its loads from L2 (16 KB + 64 BN bytes) / 64 a cycle), a tile about 1500 to start and finish, and
@@ -1364,8 +1421,8 @@ struct SmallArgs {
 // truncate their sums, as the tile product's do (kChain), so chains of 32 kU of k are summed by float32 adds.
 // For float32 outputs of more than kSmallChain of k a warp: 16 rows by 7168 -> 4096, 896 of k a warp, a
 // relative error of 8.6e-7 in one chain, 1.4e-7 in short ones, both 16 us (with SwiGLU, 8 rows: 8.4e-7 and
-// 2.5e-7, 15.4 us).  A 16-bit output's own rounding is larger by far; short chains everywhere cost 48 rows by
-// 1408 -> 2816 8.8 -> 12.7 us, in registers.
+// 2.5e-7, 15.4 us).  A 16-bit output's own rounding is larger up to a tile product's run; short chains everywhere
+// cost 48 rows by 1408 -> 2816 8.8 -> 12.7 us, in registers.
 constexpr int kSmallChain = 256;
 
 template <typename T, int kR, int kNb, bool kGated, bool kShort>
@@ -1529,7 +1586,7 @@ int launch_small(const SmallArgs &args, int type, cudaStream_t s)
                             : a.M <= 32 ? small_kernel<T, 1, 4, false, kS>
                                         : small_kernel<T, 1, 8, false, kS>);
         };
-        const bool is_short = a.epi.out_type == kTypeF32 && a.k_warp > kSmallChain;
+        const bool is_short = a.k_warp > (a.epi.out_type == kTypeF32 ? kSmallChain : kBk << run_log(type));
         auto kernel = is_short ? pick(std::true_type()) : pick(std::false_type());
         ce = cudaLaunchKernelEx(&cfg, kernel, a);
     });
@@ -1802,11 +1859,17 @@ struct Parts {
     }
 };
 
+// Workspace of a product of kb k blocks whose tiles may have more than one run of them.
+int64_t held_bytes(const Plan &p, int64_t kb, int type)
+{
+    return !p.sum && (kb + p.splits - 1) / p.splits > 1 << run_log(type) ? kHeldBytes : 0;
+}
+
 struct ForwardPlan {
     Plan p;
-    int64_t x, w, planes, bytes;
+    int64_t x, w, planes, held, bytes;
 };
-ForwardPlan plan_linear(int E, int64_t M, int N, int K, int act, bool f32)
+ForwardPlan plan_linear(int E, int64_t M, int N, int K, int act, int type, bool f32)
 {
     ForwardPlan f{};
     if (E == 0 && is_small(M, N, K, act == kActSwiglu))
@@ -1825,6 +1888,7 @@ ForwardPlan plan_linear(int E, int64_t M, int N, int K, int act, bool f32)
     f.x = ws.take(K % 8 ? M * round_up(K, 8) * 2 : 0);
     f.w = ws.take(K % 8 ? (E ? E : 1) * (int64_t)N * round_up(K, 8) * 2 : 0);
     f.planes = ws.take(f.p.splits > 1 ? f.p.splits * M * N * 4 : 0);
+    f.held = ws.take(held_bytes(f.p, kb, type));
     f.bytes = ws.at;
     return f;
 }
@@ -1832,7 +1896,7 @@ ForwardPlan plan_linear(int E, int64_t M, int N, int K, int act, bool f32)
 struct BackwardPlan {
     bool direct;
     Plan dx, dw;
-    int64_t part, dz, x, w, planes, cut_a, cut_b, bytes;
+    int64_t part, dz, x, w, planes, held, cut_a, cut_b, bytes;
 };
 BackwardPlan plan_backward(int E, int64_t M, int N, int K, int act, int type, int dout_type)
 {
@@ -1854,6 +1918,10 @@ BackwardPlan plan_backward(int E, int64_t M, int N, int K, int act, int type, in
     const int64_t px = f.dx.splits > 1 ? f.dx.splits * M * K * 4 : 0;
     const int64_t pw = f.dw.splits > 1 ? (int64_t)f.dw.splits * N * K * 4 : 0;
     f.planes = ws.take(px > pw ? px : pw);
+    // the sums of long tiles likewise; a grouped dw's depth is known on the device: at most all rows
+    const int64_t hx = M > 0 ? held_bytes(f.dx, (N + kBk - 1) / kBk, type) : 0;
+    const int64_t hw = held_bytes(f.dw, (M + kBk - 1) / kBk, type);
+    f.held = ws.take(hx > hw ? hx : hw);
     f.cut_a = ws.take((int64_t)E * kBk * ldz_of(N) * 2);
     f.cut_b = ws.take((int64_t)E * kBk * round_up(K, 8) * 2);
     f.bytes = ws.at;
@@ -1892,9 +1960,9 @@ void split_out(Gemm &g, int splits, int kb, int N, void *planes)
 
 } // namespace
 
-int64_t linear_workspace(int E, int64_t M, int N, int K, int act, int, int out_type)
+int64_t linear_workspace(int E, int64_t M, int N, int K, int act, int type, int out_type)
 {
-    return plan_linear(E, M, N, K, act, out_type == kTypeF32).bytes;
+    return plan_linear(E, M, N, K, act, type, out_type == kTypeF32).bytes;
 }
 
 int64_t linear_backward_workspace(int E, int64_t M, int N, int K, int act, int type, int dout_type)
@@ -1909,7 +1977,7 @@ int launch_linear(const LinearArgs &a, cudaStream_t s)
                           Epi{a.bias, a.residual, a.out, a.preact, a.act, a.N, a.No(), a.type, a.out_type, 0}};
         return launch_small(m, a.type, s);
     }
-    const ForwardPlan f = plan_linear(a.E, a.M, a.N, a.K, a.act, a.out_type == kTypeF32);
+    const ForwardPlan f = plan_linear(a.E, a.M, a.N, a.K, a.act, a.type, a.out_type == kTypeF32);
     char *ws = static_cast<char *>(a.ws);
     const int ld = (int)round_up(a.K, 8), experts = a.E ? a.E : 1;
     const Segments seg{a.counts, a.pad_offsets, a.E, a.M};
@@ -1925,6 +1993,7 @@ int launch_linear(const LinearArgs &a, cudaStream_t s)
     g.gated = a.act == kActSwiglu, g.act = a.act, g.fmt = a.type == kTypeBf16;
     g.bias = a.bias, g.residual = a.residual, g.out = a.out, g.preact = a.preact;
     g.type = a.type, g.out_type = a.out_type, g.vec = g.n_cols % 8 == 0;
+    g.run_log = run_log(a.type), g.held = reinterpret_cast<float4 *>(ws + f.held);
     const Epi ep = epilogue_of(g);
     const int kb = (a.K + kBk - 1) / kBk;
     split_out(g, f.p.splits, kb, a.N, ws + f.planes);
@@ -2003,6 +2072,7 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
         Gemm g{};
         g.seg = seg, g.M = (int)a.M, g.n_cols = g.N = a.K, g.K = a.N;
         g.fmt = a.type == kTypeBf16, g.out = a.dx, g.type = g.out_type = a.type, g.vec = a.K % 8 == 0;
+        g.run_log = run_log(a.type), g.held = reinterpret_cast<float4 *>(ws + f.held);
         const int kb = (a.N + kBk - 1) / kBk;
         const Epi ep = epilogue_of(g);
         split_out(g, f.dx.splits, kb, a.K, ws + f.planes);
@@ -2032,6 +2102,7 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
         Gemm g{};
         g.seg = seg, g.seg_k = 1, g.M = a.N, g.n_cols = g.N = a.K, g.K = (int)a.M;
         g.d_expert = (int64_t)a.N * a.K;
+        g.run_log = run_log(a.type), g.held = reinterpret_cast<float4 *>(ws + f.held);
         g.fmt = a.type == kTypeBf16, g.out = a.dw, g.type = g.out_type = a.type, g.vec = a.K % 8 == 0;
         const Epi ep = epilogue_of(g);
         split_out(g, f.dw.splits, (int)((a.M + kBk - 1) / kBk), a.K, ws + f.planes);

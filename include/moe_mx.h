@@ -542,7 +542,10 @@ MOE_MX_API int moe_mx_combine_backward(const void *dout, const void *grouped, in
                                        void *dgrouped, float *dtopk_w, float *dlogits, void *stream);
 
 /*
- * out = act(x w^T + bias) + residual, with float32 accumulation and one rounding of each output.
+ * out = act(x w^T + bias) + residual, with float32 accumulation and one rounding of each output.  The
+ * tensor core adds with truncation: chains of at most 512 of K for float32 outputs, 8192 for float16 and
+ * 65536 for bf16 ones (short by a ninth of half a step where all products have one sign) are joined by
+ * rounding float32 additions.
  *   num_experts  0: dense; x [rows, K], w [N, K], bias [N].
  *                E in 1..1024: the rows are in the grouped layout, w [E, N, K], bias [E, N]; counts
  *                int32 [E] and pad_offsets int32 [E+1] (device) give the segments.  NULL when dense.
@@ -571,7 +574,8 @@ MOE_MX_API int64_t moe_mx_linear_workspace(int num_experts, int64_t rows, int N,
  *   dx     [rows, K] of dtype, or NULL:     dz w (padding rows are left as they were);
  *   dw     [N, K] or [E, N, K] of dtype, or NULL: dz^T x, written (an expert without rows: zero);
  *   dbias  float32 [N] or [E, N], or NULL:  sum over the rows of dz, before dz is rounded.
- * The two products take dz rounded to dtype, the type of x and w; they accumulate in float32.
+ * The two products take dz rounded to dtype, the type of x and w; they accumulate in float32, in
+ * chains as moe_mx_linear's 16-bit outputs do.
  *   dout   [rows, N], or [rows, N/2] for SWIGLU, of dout_dtype: dtype or MOE_MX_TYPE_F32.
  *   preact as moe_mx_linear wrote it; NULL for MOE_MX_LINEAR_NONE.
  *   x, w, counts, pad_offsets, num_experts, rows, N, K, dtype, activation: as for moe_mx_linear (x is

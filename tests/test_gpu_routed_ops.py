@@ -668,3 +668,81 @@ def test_a_wait_that_gives_up_is_reported_and_harms_no_other_call():
         ops.check("cuda:0", s)
     ops.check(0, s.cuda_stream)
     assert moe_mx.moe_mx_linear_status(0) == moe_mx.MOE_MX_OK
+
+
+# ---------------------------------------------------------------- long sums
+def _positive(shape, dtype, seed, mean):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.rand(shape, generator=g, device="cuda").add_(0.5).mul_(mean)).to(dtype)
+
+
+def _ends(n, m=64):
+    return torch.arange(n, device="cuda") if n <= 2 * m else torch.cat([torch.arange(m), torch.arange(n - m, n)]).cuda()
+
+
+def _unbiased(got, want, factor=1):
+    """16-bit outputs of a long sum of one sign.  The tensor core truncates each addition of 16 products by
+    less than 2^-22 of the sum it leaves; a chain of 8192 (float16: 512 additions to a growing sum) is short by
+    at most 2^-13, one of 65536 (bf16) by 2^-10, and by half of that where the sum grows evenly: u / 8.  Chains are
+    joined in float32 and the result is rounded once, by u at most and by nothing in the mean of n values but
+    4 u / sqrt(n).  factor: how often the sum enters the output."""
+    rel = (got.to(ref.F64) - want) / want
+    u = ref.u(got.dtype)
+    assert float(rel.abs().max()) <= u + factor * u / 4 + 2.0 ** -18, f"{float(rel.abs().max()):.2e}"
+    assert abs(float(rel.mean())) <= factor * u / 8 + 4 * u / rel.numel() ** 0.5, f"mean {float(rel.mean()):.2e}"
+
+
+LONG = [  # M, N, K, act, bias and residual, preact: one round of tiles, so that k is not split
+    (40, 18944, 33280, "none", False, False), (40, 18944, 33280, "silu", True, True),
+    (200, 9471, 33281, "none", True, True), (33, 18944, 33280, "swiglu", False, True),
+    (9472, 512, 33280, "none", False, False), (9472, 512, 33280, "silu", True, True),
+    (9472, 511, 33280, "gelu", True, False), (9472, 512, 33280, "swiglu", True, True),
+    (12544, 576, 33280, "none", True, True), (18944, 128, 33280, "none", False, False),
+    (18944, 126, 33280, "swiglu", False, True), (4, 40, 1 << 20, "none", True, False),
+]
+
+
+@pytest.mark.parametrize("M,N,K,act,more,preact", LONG)
+def test_long_sums_of_16_bit_outputs(M, N, K, act, more, preact):
+    x, w = _positive((M, K), HF, 110, 0.05), _positive((N, K), HF, 111, 20 / (0.05 * K))
+    cols = N // 2 if act == "swiglu" else N
+    b = rnd((N,), F, 112) if more else None
+    res = rnd((M, cols), HF, 113) if more else None
+    pre = torch.empty(M, N, dtype=HF, device="cuda") if preact else None
+    got = ops.linear(x, w, b, residual=res, activation=act, preact=pre)
+    rows, at = _ends(M), _ends(cols)
+    wat = torch.cat([at, at + cols]) if act == "swiglu" else at
+    z = x[rows].to(ref.F64) @ w[wat].to(ref.F64).t()
+    if more:
+        z = z + b[wat].to(ref.F64)
+    want = ref.act64(z, act)
+    if more:
+        want = want + res[rows][:, at].to(ref.F64)
+    _unbiased(got[rows][:, at], want, 2 if act == "swiglu" else 1)
+    if preact:
+        _unbiased(pre[rows][:, wat], z)
+
+
+@pytest.mark.parametrize("M,N,K,dtype", [
+    (40, 33280, 18944, HF), (9472, 33280, 512, HF), (18944, 33280, 120, HF), (300000, 2048, 2304, HF),
+    (150000, 9472, 128, HF), (200000, 130, 70, HF), (600000, 2048, 2304, BF)])
+def test_long_sums_of_gradients(M, N, K, dtype):
+    d, x = _positive((M, N), dtype, 114, 0.3), _positive((M, K), dtype, 115, 2000.0 / (0.3 * M))
+    w = _positive((N, K), dtype, 116, 2000.0 / (0.3 * N))
+    dx, dw, _ = ops.linear_backward(d, x, w)
+    rows, at, n = _ends(M), _ends(K), _ends(N)
+    _unbiased(dx[rows][:, at], d[rows].to(ref.F64) @ w[:, at].to(ref.F64))
+    _unbiased(dw[n][:, at], d[:, n].to(ref.F64).t() @ x[:, at].to(ref.F64))
+
+
+def test_long_sums_of_one_experts_gradients():
+    """All rows at one of several experts: the depth of dw is known on the device alone."""
+    T, E, N, K = 70000, 3, 264, 136
+    r = ref.make_routing(T, E, 1, 117, hot=2)
+    d, x = _positive((r.rows, N), HF, 118, 0.3), _positive((r.rows, K), HF, 119, 2000.0 / (0.3 * T))
+    w = rnd((E, N, K), HF, 120)
+    _, dw, db = ops.linear_backward(d, x, w, routing=r, bias_grad=True)
+    lo, n = int(r.pad_offsets[2]), int(r.counts[2])
+    assert n == T
+    _unbiased(dw[2], d[lo:lo + n].to(ref.F64).t() @ x[lo:lo + n].to(ref.F64))
+    assert not dw[:2].abs().sum() and not db[:2].abs().sum()
