@@ -5,7 +5,9 @@
 //   z = x w^T + b          dz = dout * act'(z)
 //   out = act(z) + res     dx = dz w      dw = dz^T x      db = sum over rows of dz
 //
-// dz is rounded once to the operands' type, which the products take (db sums it before that).
+// dz is rounded once to the operands' type, which the products take (db sums it before that).  float32 dout
+// of float16 operands may lie outside float16's range, so dz is scaled by a power of two before that rounding,
+// one of each segment, and the products' sums by its inverse.
 #include "../../include/moe_mx.h"
 #include "host.cuh"
 #include "kernels.cuh"
@@ -129,6 +131,7 @@ struct Gemm {
     int act, N;           // columns of preact, and of each expert's bias
     int type, out_type, vec;
     int wide_a, wide_b;   // an M- or N-major operand of whole 64-element groups: one copy takes all of them
+    const float *unscale; // a gradient's factor of each expert's sums, or nullptr
     int64_t d_expert;     // elements from one expert's D to the next's (seg_k)
     float4 *held;         // sums of tiles of more than one run, kHeld of every epilogue warp (kHeldBytes in all)
 };
@@ -883,6 +886,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             return true;
         };
+        auto unscale = [&](uint32_t (&r)[32]) { // exact
+            if (!kPlain || !g.unscale)
+                return;
+            const float f = g.unscale[t.e];
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+                r[x] = __float_as_uint(__uint_as_float(r[x]) * f);
+        };
         while (ok && next(c)) {
             // gradients have no bias, preact, activation or residual
             const Epi ep = kPlain ? Epi{nullptr, nullptr, g.out, nullptr, kActNone, g.N, g.n_cols, g.type, g.out_type, g.vec}
@@ -1015,6 +1026,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tmem_ld32(tmem + 256u * (n & 1) + acc0 + c * 32, r);
                         tmem_wait_ld();
                         add_held(c / 2, r);
+                        unscale(r);
                         if (c + 2 >= chunks)
                             free_acc();
                         done(c, r);
@@ -1121,6 +1133,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             tmem_wait_ld();
                             add_held(c / 32, r0);
                             add_held(c / 32 + 1, r1);
+                            unscale(r0);
+                            unscale(r1);
                             if (c + 64 >= cols)
                                 free_acc();
                         }
@@ -1165,6 +1179,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_ld32(tmem + 256u * (n & 1) + lanes + col, r);
                     tmem_wait_ld();
                     add_held(chunk, r);
+                    unscale(r);
                     turn(r, f);
                 };
                 auto take_columns = [&](uint32_t col, int chunk, float (&f)[32]) {
@@ -1172,6 +1187,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_ld32(tmem + 256u * (n & 1) + lanes + col, r);
                     tmem_wait_ld();
                     add_held(chunk, r);
+                    unscale(r);
                     turn_columns(r, f);
                 };
                 for (int c = 0; c < cols; c += 32) {
@@ -1692,17 +1708,27 @@ int run_swap(Gemm &g, bool sum, const Operand &x, const Operand &w, int64_t tile
 }
 
 // ---------------------------------------------------------------- dz and the bias gradient
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+
 struct DzArgs {
     const void *dout, *preact;
-    void *dz;     // [M, ldz] or nullptr
-    float *part;  // [ceil(M / 128)][N] column sums of each 128-row block, or nullptr
+    void *dz;           // [M, ldz] or nullptr
+    float *part;        // [ceil(M / 128)][N] column sums of each 128-row block, or nullptr
+    const float *scale; // of each expert's dz, or nullptr
+    float *most;        // kMost: [ceil(M / 128)][ceil(n_out / 64)]
     Segments seg;
     int N, n_out, ldz, act;
 };
 
 // One CTA: 128 rows x 64 columns of dout (8 lanes x 8 columns, 32 row lanes x 4 rows).  The column
-// sums of a block are added in a fixed order.
-template <typename T, typename TO, int V> __global__ void __launch_bounds__(256) dz_kernel(const DzArgs a)
+// sums of a block are added in a fixed order.  kMost: nothing but the largest finite |dz| of the block.
+template <typename T, typename TO, int V, bool kMost> __global__ void __launch_bounds__(256) dz_kernel(const DzArgs a)
 {
     __shared__ float red[32][65];
     const int64_t m0 = (int64_t)blockIdx.x * 128;
@@ -1715,7 +1741,9 @@ template <typename T, typename TO, int V> __global__ void __launch_bounds__(256)
         return; // a block of padding, or past the last segment
     const bool gated = a.act == kActSwiglu;
     const int cl = threadIdx.x % 8, rl = threadIdx.x / 8;
-    float sum[2][8] = {};
+    const float scale = !kMost && a.scale ? a.scale[e] : 1.f;
+    float sum[2][8] = {}, most = 0.f;
+    auto finite = [](float v) { return fabsf(v) <= 3.402823466e38f ? fabsf(v) : 0.f; };
     for (int v = 0; v < 8; v += V) {
         const int n = blockIdx.y * 64 + cl * 8 + v;
         if (n >= a.n_out)
@@ -1739,7 +1767,7 @@ template <typename T, typename TO, int V> __global__ void __launch_bounds__(256)
             const int64_t m = m0 + i * 32 + rl;
             if (m >= end)
                 continue;
-            float d[V], z[V], u[V], dz[V], du[V];
+            float d[V], z[V], u[V], dz[V], du[V] = {};
             rd[i].get(d);
             if (gated) {
                 rz[i].get(z);
@@ -1761,13 +1789,33 @@ template <typename T, typename TO, int V> __global__ void __launch_bounds__(256)
                     sum[0][v + q] += dz[q];
                 }
             }
-            if (a.dz) {
+            if (kMost) {
+#pragma unroll
+                for (int q = 0; q < V; ++q)
+                    most = fmaxf(most, gated ? fmaxf(finite(dz[q]), finite(du[q])) : finite(dz[q]));
+            } else if (a.dz) {
                 T *o = static_cast<T *>(a.dz) + m * a.ldz + n;
+#pragma unroll
+                for (int q = 0; q < V; ++q)
+                    dz[q] *= scale, du[q] *= scale;
                 Raw<T, V>::put(o, dz);
                 if (gated)
                     Raw<T, V>::put(o + a.n_out, du);
             }
         }
+    }
+    if (kMost) {
+        __shared__ float largest[8];
+        const float m = warp_max(most);
+        if (threadIdx.x % 32 == 0)
+            largest[threadIdx.x / 32] = m;
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            const float b = warp_max(threadIdx.x < 8 ? largest[threadIdx.x] : 0.f);
+            if (threadIdx.x == 0)
+                a.most[(size_t)blockIdx.x * gridDim.y + blockIdx.y] = b;
+        }
+        return;
     }
     if (!a.part)
         return;
@@ -1785,6 +1833,38 @@ template <typename T, typename TO, int V> __global__ void __launch_bounds__(256)
                 a.part[(size_t)blockIdx.x * a.N + h * a.n_out + n] = t;
         }
         __syncthreads();
+    }
+}
+
+// The power of two that takes a segment's largest finite |dz| to [2^14, 2^15), and its inverse (after all
+// experts' scales): float16 then holds to half a step what is down to 2^-28 of the largest, and the rest to
+// 2^-39 of it, whatever the range of dout.  One CTA per expert over its blocks' maxima.
+__global__ void __launch_bounds__(1024) scale_kernel(const float *block_most, int per_block, Segments seg, float *scale)
+{
+    grid_dep_wait();
+    grid_dep_launch();
+    __shared__ float largest[32];
+    const int e = blockIdx.x;
+    int first = 0;
+    const int64_t rows = seg.E ? segment_rows(seg, e, first) : seg.M;
+    const int64_t n = (rows + 127) / 128 * per_block;
+    const float *p = block_most + (size_t)(first / 128) * per_block;
+    float m = 0.f;
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < n; i += 1024)
+        m = fmaxf(m, p[i]);
+    m = warp_max(m);
+    if (threadIdx.x % 32 == 0)
+        largest[threadIdx.x / 32] = m;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        m = warp_max(largest[threadIdx.x]);
+        if (threadIdx.x == 0) {
+            const int exponent = (int)(__float_as_uint(m) >> 23) - 127; // -127: zero or subnormal
+            const int up = m == 0.f ? 0 : min(14 - exponent, 126);      // 14 - 127 at least
+            scale[e] = __uint_as_float((uint32_t)(127 + up) << 23);
+            scale[gridDim.x + e] = __uint_as_float((uint32_t)(127 - up) << 23);
+        }
     }
 }
 
@@ -1896,8 +1976,10 @@ ForwardPlan plan_linear(int E, int64_t M, int N, int K, int act, int type, bool 
 struct BackwardPlan {
     bool direct;
     Plan dx, dw;
-    int64_t part, dz, x, w, planes, held, cut_a, cut_b, bytes;
+    int64_t part, most, scale, dz, x, w, planes, held, cut_a, cut_b, bytes;
 };
+bool dz_is_scaled(int type, int dout_type) { return type == kTypeF16 && dout_type == kTypeF32; }
+
 BackwardPlan plan_backward(int E, int64_t M, int N, int K, int act, int type, int dout_type)
 {
     BackwardPlan f{};
@@ -1911,6 +1993,9 @@ BackwardPlan plan_backward(int E, int64_t M, int N, int K, int act, int type, in
     }
     Parts ws;
     f.part = ws.take((M + 127) / 128 * N * 4);
+    const bool scaled = dz_is_scaled(type, dout_type);
+    f.most = ws.take(scaled ? (M + 127) / 128 * (((act == kActSwiglu ? N / 2 : N) + 63) / 64) * 4 : 0);
+    f.scale = ws.take(scaled ? 2 * (E ? E : 1) * 4 : 0);
     f.dz = ws.take(f.direct ? 0 : M * ldz_of(N) * 2);
     f.x = ws.take(K % 8 ? M * round_up(K, 8) * 2 : 0);
     f.w = ws.take(K % 8 ? (E ? E : 1) * (int64_t)N * round_up(K, 8) * 2 : 0);
@@ -2029,13 +2114,27 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
     d.part = a.dbias ? part : nullptr;
     if (!f.direct && (a.dx || a.dw))
         d.dz = ws + f.dz;
+    const int experts = a.E ? a.E : 1;
+    const float *unscale = nullptr;
     if (a.M > 0 && (d.part || d.dz)) {
         const dim3 grid((unsigned)((a.M + 127) / 128), (d.n_out + 63) / 64);
+        const bool vec = d.n_out % 8 == 0;
+        if (d.dz && dz_is_scaled(a.type, a.dout_type)) {
+            float *scale = reinterpret_cast<float *>(ws + f.scale);
+            d.most = reinterpret_cast<float *>(ws + f.most);
+            cudaError_t ce = launch_kernel(vec ? dz_kernel<__half, float, 8, true> : dz_kernel<__half, float, 1, true>,
+                                           grid, dim3(256), 0, s, true, d);
+            if (ce == cudaSuccess)
+                ce = launch_kernel(scale_kernel, dim3(experts), dim3(1024), 0, s, true, d.most, (int)grid.y, seg, scale);
+            if (ce != cudaSuccess)
+                return cuda_fail(ce, "gradient scale launch");
+            d.scale = scale, unscale = scale + experts;
+        }
         by_half(a.type, [&](auto x) {
             using T = decltype(x);
             auto go = [&](auto y) {
                 using TO = decltype(y);
-                launch_kernel(d.n_out % 8 == 0 ? dz_kernel<T, TO, 8> : dz_kernel<T, TO, 1>, grid, dim3(256), 0, s, true, d);
+                launch_kernel(vec ? dz_kernel<T, TO, 8, false> : dz_kernel<T, TO, 1, false>, grid, dim3(256), 0, s, true, d);
             };
             if (a.dout_type == kTypeF32)
                 go(float());
@@ -2044,7 +2143,7 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
         });
     }
     const void *dz = f.direct ? a.dout : d.dz;
-    const int ldz = f.direct ? a.N : d.ldz, ldk = (int)round_up(a.K, 8), experts = a.E ? a.E : 1;
+    const int ldz = f.direct ? a.N : d.ldz, ldk = (int)round_up(a.K, 8);
     // x and w with aligned rows, where a product reads them
     const void *xk = a.dw && a.M > 0 ? a.x : nullptr, *wk = a.dx && a.M > 0 ? a.w : nullptr;
     cudaError_t pe = launch_pack(xk, a.M, seg, ws + f.x, wk, (int64_t)experts * a.N, ws + f.w, a.K, s);
@@ -2072,7 +2171,7 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
         Gemm g{};
         g.seg = seg, g.M = (int)a.M, g.n_cols = g.N = a.K, g.K = a.N;
         g.fmt = a.type == kTypeBf16, g.out = a.dx, g.type = g.out_type = a.type, g.vec = a.K % 8 == 0;
-        g.run_log = run_log(a.type), g.held = reinterpret_cast<float4 *>(ws + f.held);
+        g.run_log = run_log(a.type), g.held = reinterpret_cast<float4 *>(ws + f.held), g.unscale = unscale;
         const int kb = (a.N + kBk - 1) / kBk;
         const Epi ep = epilogue_of(g);
         split_out(g, f.dx.splits, kb, a.K, ws + f.planes);
@@ -2102,7 +2201,7 @@ int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s)
         Gemm g{};
         g.seg = seg, g.seg_k = 1, g.M = a.N, g.n_cols = g.N = a.K, g.K = (int)a.M;
         g.d_expert = (int64_t)a.N * a.K;
-        g.run_log = run_log(a.type), g.held = reinterpret_cast<float4 *>(ws + f.held);
+        g.run_log = run_log(a.type), g.held = reinterpret_cast<float4 *>(ws + f.held), g.unscale = unscale;
         g.fmt = a.type == kTypeBf16, g.out = a.dw, g.type = g.out_type = a.type, g.vec = a.K % 8 == 0;
         const Epi ep = epilogue_of(g);
         split_out(g, f.dw.splits, (int)((a.M + kBk - 1) / kBk), a.K, ws + f.planes);

@@ -575,7 +575,9 @@ MOE_MX_API int64_t moe_mx_linear_workspace(int num_experts, int64_t rows, int N,
  *   dw     [N, K] or [E, N, K] of dtype, or NULL: dz^T x, written (an expert without rows: zero);
  *   dbias  float32 [N] or [E, N], or NULL:  sum over the rows of dz, before dz is rounded.
  * The two products take dz rounded to dtype, the type of x and w; they accumulate in float32, in
- * chains as moe_mx_linear's 16-bit outputs do.
+ * chains as moe_mx_linear's 16-bit outputs do.  float32 dout with float16 operands: dz is scaled before that
+ * rounding by a power of two, for each expert (or the dense call) the one that takes its largest finite value
+ * to [2^14, 2^15), and the sums by its inverse, so that dout need not lie in float16's range.
  *   dout   [rows, N], or [rows, N/2] for SWIGLU, of dout_dtype: dtype or MOE_MX_TYPE_F32.
  *   preact as moe_mx_linear wrote it; NULL for MOE_MX_LINEAR_NONE.
  *   x, w, counts, pad_offsets, num_experts, rows, N, K, dtype, activation: as for moe_mx_linear (x is

@@ -746,3 +746,74 @@ def test_long_sums_of_one_experts_gradients():
     assert n == T
     _unbiased(dw[2], d[lo:lo + n].to(ref.F64).t() @ x[lo:lo + n].to(ref.F64))
     assert not dw[:2].abs().sum() and not db[:2].abs().sum()
+
+
+# ---------------------------------------------------------------- float32 gradients of float16 operands
+@pytest.mark.parametrize("size,act", [(1e-7, "none"), (1e-6, "swiglu"), (3e-9, "silu"), (1e6, "none"), (2e5, "gelu"),
+                                      (1e-40, "none")])
+@pytest.mark.parametrize("M,N,K", [(1000, 384, 264), (130, 66, 70), (3, 40, 24)])
+def test_float32_gradients_outside_float16s_range(M, N, K, size, act):
+    """x and w of a size that brings dx and dw into float16's range; two roundings, of dz and of the result."""
+    back = min(1 / size, 2.0 ** 12) if size < 1 else max(1 / size, 2.0 ** -13)
+    x, w = rnd((M, K), HF, 130, back), rnd((N, K), HF, 131, back)
+    cols = N // 2 if act == "swiglu" else N
+    d = rnd((M, cols), F, 132, size)
+    pre = rnd((M, N), HF, 133) if act != "none" else None
+    dx, dw, db = ops.linear_backward(d, x, w, pre, act, bias_grad=True)
+    want, _ = ref.linear_backward64(d, x, w, pre, act)
+    small = 2.0 ** -25  # half a subnormal step of the results
+    for g, t, name in ((dx, want[0], "dx"), (dw, want[1], "dw")):
+        assert g.isfinite().all(), name
+        err = float((g.to(ref.F64) - t).norm())
+        tol = (math.sqrt(2) * ref.u(HF) + 2.0 ** -16) * float(t.norm()) + small * t.numel() ** 0.5
+        assert err <= tol, f"{name}: {err / float(t.norm()):.2e}"
+    rel = float((db.to(ref.F64) - want[2]).norm() / want[2].norm())
+    assert rel <= (2.0 ** -16 if size > 1e-38 else 1e-4), f"db: {rel:.2e}"  # float32 itself is subnormal there
+
+
+def test_float32_gradients_of_experts_of_different_sizes():
+    """Each expert's gradients are scaled by its own largest value; an infinity or NaN in one row spoils that
+    row of dx and its expert's dw alone, and no finite value near it."""
+    T, E, N, K = 500, 6, 136, 200
+    r = ref.make_routing(T, E, 2, 140)
+    d = rnd((r.rows, N), F, 141)
+    x, w = rnd((r.rows, K), HF, 142), rnd((E, N, K), HF, 143)
+    pad = torch.ones(r.rows, dtype=torch.bool, device="cuda")
+    for e, lo, hi in ref.segments(r, r.rows):
+        size = 10.0 ** (3 * (e - 3))  # 1e-9 .. 1e6
+        d[lo:hi] *= size
+        x[lo:hi] *= min(max(1 / size, 2.0 ** -13), 2.0 ** 12)
+        w[e] *= min(max(1 / size, 2.0 ** -13), 2.0 ** 12)
+        pad[lo:hi] = False
+    d[pad], x[pad] = math.nan, math.nan
+    def check(dx, dw, skip=None):
+        (tx, tw, _), _ = ref.linear_backward64(d, x, w, None, "none", r)
+        for e, lo, hi in ref.segments(r, r.rows):
+            if hi == lo:
+                continue
+            rows = [i for i in range(lo, hi) if i != skip]
+            for g, t in ((dx[rows], tx[rows]), (dw[e], tw[e])):
+                if not t.isfinite().all():
+                    continue
+                tol = (math.sqrt(2) * ref.u(HF) + 2.0 ** -16) * float(t.norm()) + 2.0 ** -25 * t.numel() ** 0.5
+                assert float((g.to(ref.F64) - t).norm()) <= tol, e
+    dx, dw, _ = ops.linear_backward(d, x, w, routing=r)
+    again = ops.linear_backward(d, x, w, routing=r)
+    assert torch.equal(dx[~pad], again[0][~pad]) and torch.equal(dw, again[1])
+    check(dx, dw)
+    lo = int(r.pad_offsets[4])
+    d[lo, 0] = math.inf
+    dx, dw, _ = ops.linear_backward(d, x, w, routing=r)
+    check(dx, dw, lo)
+    assert not dx[lo].isfinite().any() and not dw[4, 0].isfinite().any() and dw[4, 1:].isfinite().all()
+
+
+def test_float32_gradients_of_rows_of_different_sizes():
+    """Rows of one segment 2^20 apart keep their relative precision."""
+    M, N, K = 64, 256, 128
+    d = rnd((M, N), F, 150, 1e-3) * 2.0 ** -(torch.arange(M, device="cuda") % 21)[:, None]
+    x, w = rnd((M, K), HF, 151), rnd((N, K), HF, 152, 1000.0)
+    dx = ops.linear_backward(d, x, w, weight_grad=False)[0]
+    want = d.to(ref.F64) @ w.to(ref.F64)
+    err, size = (dx.to(ref.F64) - want).norm(dim=1), want.norm(dim=1)
+    assert bool((err <= (math.sqrt(2) * ref.u(HF) + 2.0 ** -16) * size + 2.0 ** -25 * K ** 0.5).all())
