@@ -1251,7 +1251,7 @@ __global__ void __launch_bounds__(256) reduce_kernel(const float *planes, int sp
 {
     grid_dep_wait();
     grid_dep_launch();
-    const uint32_t i = blockIdx.x * 256 + threadIdx.x; // a split product has fewer tiles than there are pairs
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x; // plan_dense splits products of less than 2^31 values alone
     const uint32_t m = i / (uint32_t)g.n_cols, n = i % (uint32_t)g.n_cols;
     if (m >= (uint32_t)M)
         return;
@@ -1365,6 +1365,7 @@ struct Plan {
     bool sum;  // the sum over chains of kChain k blocks kept in registers (at most 192 columns, or 128 tokens)
     int tok;   // kSwap: tokens of a tile; else 0
 };
+constexpr int64_t kMostSplit = (int64_t)1 << 31; // reduce_kernel counts the values of D in 32 bits
 Plan plan_dense(int64_t M, int cols, int kb, bool gated, bool mn, bool f32, bool swap)
 {
     Plan best{256, 1, false, 0};
@@ -1373,7 +1374,7 @@ Plan plan_dense(int64_t M, int cols, int kb, bool gated, bool mn, bool f32, bool
     double best_t = 1e30;
     auto consider = [&](int bn, int tok, int64_t row_tiles, int col_tiles, int width) {
         for (int s : {1, 2, 3, 4, 6, 8, 12, 18, 24, 36}) {
-            if (s > 1 && kb / s < 3)
+            if (s > 1 && (kb / s < 3 || M * cols >= kMostSplit))
                 break;
             const int64_t kbs = (kb + s - 1) / s;
             const bool sum = f32 && kbs > kChain;

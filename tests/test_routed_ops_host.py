@@ -139,3 +139,12 @@ def test_watchdog_and_check_refuse(lib):
     assert lib.moe_mx_debug_linear_watchdog(-1, 1000, None) in (BAD, moe_mx.MOE_MX_ERR_CUDA)
     with pytest.raises(ValueError, match="CUDA device"):
         ops.check("cpu")
+
+
+def test_products_of_2_to_the_31_values_are_not_split(lib):
+    """The sum of a split product's planes counts values in 32 bits: none of that size has planes."""
+    for M, N in ((1 << 15, 1 << 16), ((1 << 15) + 1, 1 << 16), (74 * 256 + 1, 116000), ((1 << 20) + 3, 2049)):
+        for K in (1 << 13, 1 << 17, 1 << 20):
+            assert M * N >= 1 << 31
+            assert lib.moe_mx_linear_workspace(0, M, N, K, 0, 0, 0) < 4 * M * N
+    assert lib.moe_mx_linear_workspace(0, 2048, 2560, 14336, 0, 0, 0) >= 2 * 4 * 2048 * 2560  # split, in 240 tiles
