@@ -60,6 +60,25 @@ bool overlap(const void *p, size_t n, const void *q, size_t m)
     return p && q && n && m && a < b + m && b < a + n;
 }
 
+struct Range {
+    const void *p;
+    size_t n;
+};
+
+// One of outs overlaps another of them or one of ins.
+template <int O, int I> bool clash(const Range (&outs)[O], const Range (&ins)[I])
+{
+    for (int i = 0; i < O; ++i) {
+        for (const Range &r : ins)
+            if (overlap(outs[i].p, outs[i].n, r.p, r.n))
+                return true;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
+                return true;
+    }
+    return false;
+}
+
 struct LinearSizes {
     int64_t rows;
     int E, N, K, act;
@@ -133,8 +152,10 @@ int moe_mx_dispatch(const void *x, int num_tokens, int hidden, int top_k, const 
     if ((rc = device_of(x, "x", &dev)) ||
         (rc = check_ptr(pos_of_pair, dev, "pos_of_pair")) || (rc = check_ptr(grouped, dev, "grouped")))
         return rc;
-    if (overlap(x, (size_t)num_tokens * hidden * type_bytes(dtype), grouped, (size_t)rows * hidden * type_bytes(dtype)))
-        return fail(MOE_MX_ERR_INVALID_ARG, "grouped must not overlap x");
+    const size_t T = num_tokens, row = (size_t)hidden * type_bytes(dtype);
+    const Range outs[] = {{grouped, rows * row}}, ins[] = {{x, T * row}, {pos_of_pair, T * top_k * 4}};
+    if (clash(outs, ins))
+        return fail(MOE_MX_ERR_INVALID_ARG, "grouped must not overlap x or pos_of_pair");
     const DeviceGuard guard(dev);
     PermuteArgs a{};
     a.T = num_tokens, a.H = hidden, a.k = top_k, a.rows = rows, a.pos = pos_of_pair, a.type = dtype;
@@ -159,9 +180,11 @@ int moe_mx_combine(const void *grouped, int64_t rows, int num_tokens, int hidden
         (rc = check_ptr(grouped, dev, "grouped")) || (rc = check_ptr(pos_of_pair, dev, "pos_of_pair")) ||
         (topk_w && (rc = check_ptr(topk_w, dev, "topk_w"))))
         return rc;
-    if (overlap(grouped, (size_t)rows * hidden * type_bytes(dtype), out,
-                (size_t)num_tokens * hidden * type_bytes(out_dtype)))
-        return fail(MOE_MX_ERR_INVALID_ARG, "out must not overlap grouped");
+    const size_t T = num_tokens, pairs = T * top_k * 4;
+    const Range outs[] = {{out, T * hidden * type_bytes(out_dtype)}},
+                ins[] = {{grouped, (size_t)rows * hidden * type_bytes(dtype)}, {pos_of_pair, pairs}, {topk_w, pairs}};
+    if (clash(outs, ins))
+        return fail(MOE_MX_ERR_INVALID_ARG, "out must not overlap grouped, pos_of_pair or topk_w");
     const DeviceGuard guard(dev);
     PermuteArgs a{};
     a.T = num_tokens, a.H = hidden, a.k = top_k, a.rows = rows, a.pos = pos_of_pair, a.w = topk_w;
@@ -195,10 +218,14 @@ int moe_mx_combine_backward(const void *dout, const void *grouped, int64_t rows,
         (dtopk_w && (rc = check_ptr(dtopk_w, dev, "dtopk_w"))) ||
         (dlogits && ((rc = check_ptr(dlogits, dev, "dlogits")) || (rc = check_ptr(topk_ids, dev, "topk_ids")))))
         return rc;
-    const size_t g_bytes = (size_t)rows * hidden * type_bytes(dtype);
-    if (overlap(dgrouped, g_bytes, dout, (size_t)num_tokens * hidden * type_bytes(dout_dtype)) ||
-        ((dtopk_w || dlogits) && overlap(dgrouped, g_bytes, grouped, g_bytes)))
-        return fail(MOE_MX_ERR_INVALID_ARG, "dgrouped must not overlap dout or grouped");
+    const bool dots = dtopk_w || dlogits;
+    const size_t T = num_tokens, pairs = T * top_k * 4, g_bytes = (size_t)rows * hidden * type_bytes(dtype);
+    const Range outs[] = {{dgrouped, g_bytes}, {dtopk_w, pairs}, {dlogits, T * num_experts * 4}},
+                ins[] = {{dout, T * hidden * type_bytes(dout_dtype)}, {dots ? grouped : nullptr, g_bytes},
+                         {pos_of_pair, pairs}, {dtopk_w == topk_w ? nullptr : topk_w, pairs}, {dlogits ? topk_ids : nullptr, pairs}};
+    if (clash(outs, ins))
+        return fail(MOE_MX_ERR_INVALID_ARG, "dgrouped, dtopk_w and dlogits must not overlap each other, dout, grouped "
+                                            "or the routing (dtopk_w may be topk_w itself)");
     const DeviceGuard guard(dev);
     PermuteArgs a{};
     a.T = num_tokens, a.H = hidden, a.k = top_k, a.rows = rows, a.pos = pos_of_pair, a.w = topk_w, a.ids = topk_ids;
@@ -237,21 +264,22 @@ int moe_mx_linear(const void *x, const void *w, const float *bias, const void *r
     if (rc || rows == 0)
         return rc;
     int dev;
+    const int64_t need = linear_workspace(num_experts, rows, N, K, activation, dtype, out_dtype);
     if ((rc = device_of(x, "x", &dev)) || (rc = check_ptr(w, dev, "w")) ||
         (rc = check_ptr(out, dev, "out")) || (bias && (rc = check_ptr(bias, dev, "bias"))) ||
         (residual && (rc = check_ptr(residual, dev, "residual"))) ||
         (preact && (rc = check_ptr(preact, dev, "preact"))) ||
         (rc = check_routing(counts, pad_offsets, num_experts, dev)) ||
-        (rc = check_workspace(workspace, workspace_bytes,
-                              linear_workspace(num_experts, rows, N, K, activation, dtype, out_dtype), dev)))
+        (rc = check_workspace(workspace, workspace_bytes, need, dev)))
         return rc;
-    const size_t xb = (size_t)rows * K * 2, wb = z.slots() * N * K * 2, ob = (size_t)rows * z.No() * type_bytes(out_dtype),
-                 pb = preact ? (size_t)rows * N * 2 : 0;
-    if (overlap(out, ob, x, xb) || overlap(out, ob, w, wb) || overlap(out, ob, preact, pb) ||
-        overlap(preact, pb, x, xb) || overlap(preact, pb, w, wb) || overlap(preact, pb, residual, ob) ||
-        (residual != out && overlap(out, ob, residual, ob)))
-        return fail(MOE_MX_ERR_INVALID_ARG,
-                    "out and preact must not overlap x, w, each other or residual (out may be residual itself)");
+    const size_t ob = (size_t)rows * z.No() * type_bytes(out_dtype);
+    const Range outs[] = {{out, ob}, {preact, (size_t)rows * N * 2}, {workspace, (size_t)need}},
+                ins[] = {{x, (size_t)rows * K * 2}, {w, z.slots() * N * K * 2}, {bias, z.slots() * N * 4},
+                         {residual == out ? nullptr : residual, ob}, {counts, (size_t)num_experts * 4},
+                         {pad_offsets, ((size_t)num_experts + 1) * 4}};
+    if (clash(outs, ins))
+        return fail(MOE_MX_ERR_INVALID_ARG, "out, preact and workspace must not overlap each other, x, w, bias, residual "
+                                            "(out may be residual itself) or the routing");
     const DeviceGuard guard(dev);
     LinearArgs a{};
     a.M = rows, a.N = N, a.K = K, a.E = num_experts, a.type = dtype, a.out_type = out_dtype, a.act = activation;
@@ -299,6 +327,7 @@ int moe_mx_linear_backward(const void *dout, const void *x, const void *w, const
     if (activation != MOE_MX_LINEAR_NONE && !preact && rows > 0)
         return fail(MOE_MX_ERR_INVALID_ARG, "preact must be given for an activation");
     int dev;
+    const int64_t need = linear_backward_workspace(num_experts, rows, N, K, activation, dtype, dout_dtype);
     const bool some = rows > 0; // with no rows only the zero gradients dw and dbias are written
     if (some && ((rc = device_of(dout, "dout", &dev))))
         return rc;
@@ -313,24 +342,16 @@ int moe_mx_linear_backward(const void *dout, const void *x, const void *w, const
         (some && dx && (rc = check_ptr(dx, dev, "dx"))) || (dw && (rc = check_ptr(dw, dev, "dw"))) ||
         (dbias && (rc = check_ptr(dbias, dev, "dbias"))) ||
         (rc = check_routing(counts, pad_offsets, num_experts, dev)) ||
-        (rc = check_workspace(workspace, workspace_bytes,
-                              linear_backward_workspace(num_experts, rows, N, K, activation, dtype, dout_dtype), dev)))
+        (rc = check_workspace(workspace, workspace_bytes, need, dev)))
         return rc;
-    const size_t xb = (size_t)rows * K * 2, wb = z.slots() * N * K * 2,
-                 db = (size_t)rows * z.No() * type_bytes(dout_dtype), pb = preact ? (size_t)rows * N * 2 : 0,
-                 bb = z.slots() * N * 4;
-    const void *in[4] = {dout, x, w, preact};
-    const size_t in_b[4] = {db, xb, wb, pb};
-    const void *outs[3] = {dx, dw, dbias};
-    const size_t out_b[3] = {xb, wb, bb};
-    for (int i = 0; i < 3; ++i) {
-        for (int j = 0; j < 4; ++j)
-            if (overlap(outs[i], out_b[i], in[j], in_b[j]))
-                return fail(MOE_MX_ERR_INVALID_ARG, "dx, dw and dbias must not overlap dout, x, w or preact");
-        for (int j = 0; j < i; ++j)
-            if (overlap(outs[i], out_b[i], outs[j], out_b[j]))
-                return fail(MOE_MX_ERR_INVALID_ARG, "dx, dw and dbias must not overlap each other");
-    }
+    const size_t xb = (size_t)rows * K * 2, wb = z.slots() * N * K * 2;
+    const Range outs[] = {{dx, xb}, {dw, wb}, {dbias, z.slots() * N * 4}, {workspace, (size_t)need}},
+                ins[] = {{dout, (size_t)rows * z.No() * type_bytes(dout_dtype)}, {x, xb}, {w, wb},
+                         {preact, (size_t)rows * N * 2}, {counts, (size_t)num_experts * 4},
+                         {pad_offsets, ((size_t)num_experts + 1) * 4}};
+    if (clash(outs, ins))
+        return fail(MOE_MX_ERR_INVALID_ARG, "dx, dw, dbias and workspace must not overlap each other, dout, x, w, preact "
+                                            "or the routing");
     const DeviceGuard guard(dev);
     LinearBackwardArgs a{};
     a.M = rows, a.N = N, a.K = K, a.E = num_experts, a.type = dtype, a.dout_type = dout_dtype, a.act = activation;

@@ -480,7 +480,8 @@ MOE_MX_API int moe_mx_route_group_noalloc(const float *router_logits, int num_to
  * They need no handle, allocate nothing, keep nothing between calls that a later one uses, and may be
  * captured in a CUDA graph.  A call runs on the device that holds its first tensor; `stream` is a stream of that
  * device.  Calls on different streams do not disturb one another as long as their output and
- * workspace buffers differ.  No atomics: equal inputs give equal bits.
+ * workspace buffers differ.  No atomics: equal inputs give equal bits.  What a call writes, its
+ * workspace included, overlaps nothing else that it is given, unless stated otherwise (INVALID_ARG).
  *
  * Grouped layout: grouped buffers have `rows` rows (at least pad_offsets[E]); expert e's rows are
  * pad_offsets[e] .. pad_offsets[e] + counts[e] - 1, pad_offsets[e] being multiples of 128 in
@@ -504,7 +505,7 @@ MOE_MX_API int moe_mx_route_group_noalloc(const float *router_logits, int num_to
  *   x            [T, H] of dtype (any MOE_MX_TYPE_*); T = 0 enqueues nothing.
  *   pos_of_pair  int32 [T*k] grouped row of each pair, all different; a row outside [0, rows) (a
  *                pair of another shard's expert) is left out.
- *   grouped      [rows, H] of dtype; only the pairs' rows are written.  Must not overlap x.
+ *   grouped      [rows, H] of dtype; only the pairs' rows are written.
  * The gradient of dispatch is moe_mx_combine without weights.
  * Errors: INVALID_ARG, CUDA.
  */
@@ -515,7 +516,7 @@ MOE_MX_API int moe_mx_dispatch(const void *x, int num_tokens, int hidden, int to
  * Grouped rows back to their tokens: out[t] = sum_j topk_w[t,j] * grouped[pos_of_pair[t*k + j]], j
  * ascending, in float32, rounded once.
  *   grouped   [rows, H] of dtype; out [T, H] of out_dtype, written (a token without a pair in
- *             [0, rows): zero).  out must not overlap grouped.
+ *             [0, rows): zero).
  *   topk_w    float32 [T, k], or NULL: every weight 1 (the gradient of dispatch).
  * Errors: INVALID_ARG, CUDA.
  */
@@ -526,8 +527,9 @@ MOE_MX_API int moe_mx_combine(const void *grouped, int64_t rows, int num_tokens,
 /*
  * Gradient of moe_mx_combine with weights, and of the router's weights.  With r = pos_of_pair[t*k + j]:
  *   dgrouped [rows, H] of dtype, or NULL:  dgrouped[r] = topk_w[t,j] * dout[t] (padding rows are left
- *            as they were); must not overlap dout or grouped.
- *   dtopk_w  float32 [T, k], or NULL:      <dout[t], grouped[r]> (0 for a pair left out).
+ *            as they were); may be grouped itself when nothing else is asked for.
+ *   dtopk_w  float32 [T, k], or NULL:      <dout[t], grouped[r]> (0 for a pair left out); may be topk_w
+ *            itself.
  *   dlogits  float32 [T, num_experts], or NULL: the gradient through topk_w = softmax over the k chosen
  *            logits, which is what the router computes: dlogits[t, topk_ids[t,j]] = topk_w[t,j] *
  *            (dtopk_w[t,j] - sum_i topk_w[t,i] dtopk_w[t,i]), 0 for an expert not chosen (an id outside

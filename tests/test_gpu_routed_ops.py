@@ -817,3 +817,47 @@ def test_float32_gradients_of_rows_of_different_sizes():
     want = d.to(ref.F64) @ w.to(ref.F64)
     err, size = (dx.to(ref.F64) - want).norm(dim=1), want.norm(dim=1)
     assert bool((err <= (math.sqrt(2) * ref.u(HF) + 2.0 ** -16) * size + 2.0 ** -25 * K ** 0.5).all())
+
+
+def test_outputs_over_any_input_are_refused():
+    M, N, K, E, k = 4, 64, 68, 4, 2
+    x, w, b = rnd((M, K), BF, 160), rnd((N, K), BF, 161), rnd((M, N), F, 162)
+    with pytest.raises(moe_mx.MoeMxError, match="overlap"):
+        ops.linear(x, w, b[0], out=b)
+    with pytest.raises(moe_mx.MoeMxError, match="overlap"):
+        ops.linear(x, w, b[0], preact=b.view(-1).view(BF)[:M * N].view(M, N))
+    need = moe_mx.moe_mx_linear_workspace(0, M, N, K, 0, 0, 0)
+    assert need > 0
+    big = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for name in ("x", "w", "out"):
+        t = {"x": x, "w": w, "out": torch.empty(M, N, dtype=BF, device="cuda")}
+        t[name] = big
+        with pytest.raises(moe_mx.MoeMxError, match="workspace.*overlap"):
+            moe_mx.moe_mx_linear(t["x"], t["w"], None, None, None, None, 0, M, N, K, 0, 0, 0, t["out"], None, big, need)
+    need = moe_mx.moe_mx_linear_backward_workspace(0, M, N, K, 0, 0, 0)
+    big, dw = torch.zeros(need, dtype=torch.uint8, device="cuda"), torch.empty_like(w)
+    d = rnd((M, N), BF, 163)
+    for args in ((big, x, w, None, dw), (d, x, big, torch.empty_like(x), None), (d, x, w, None, big)):
+        with pytest.raises(moe_mx.MoeMxError, match="workspace.*overlap"):
+            moe_mx.moe_mx_linear_backward(*args[:3], None, None, None, 0, M, N, K, 0, 0, 0, args[3], args[4], None, big, need)
+    # the routing of the permutes
+    r = ref.make_routing(M, E, k, 164)
+    buf = torch.zeros(r.rows, 8, dtype=F, device="cuda")
+    xs = rnd((M, 8), F, 165)
+    with pytest.raises(moe_mx.MoeMxError, match="overlap"):
+        ops.dispatch(xs, r._replace(pos_of_pair=buf.view(torch.int32).view(-1)[:M * k]), out=buf)
+    with pytest.raises(moe_mx.MoeMxError, match="overlap"):
+        ops.combine(rnd((r.rows, 8), F, 166), r._replace(topk_w=buf.view(-1)[:M * k].view(M, k)), out=buf[:M])
+    with pytest.raises(moe_mx.MoeMxError, match="overlap"):
+        ops.combine_backward(xs, rnd((r.rows, 8), F, 167), r._replace(topk_w=buf.view(-1)[:M * k].view(M, k)), dy=buf)
+    assert not buf.any() and not big.any()
+    # out may be the residual itself, and what a call does not touch may lie anywhere
+    ops.linear(x, w, residual=d, out=d)
+    ops.combine_backward(xs, rnd((r.rows, 8), F, 168), r, dy=buf)
+    y = rnd((r.rows, 8), F, 169)
+    want = ops.combine_backward(xs, y, r)
+    both = r.topk_w.clone()
+    moe_mx.moe_mx_combine_backward(xs, y, r.rows, M, 8, k, r.pos_of_pair, both, None, 0, 1, 1, None, both, None)
+    assert torch.equal(both, want[1])
+    moe_mx.moe_mx_combine_backward(xs, y, r.rows, M, 8, k, r.pos_of_pair, r.topk_w, None, 0, 1, 1, y, None, None)
+    assert torch.equal(y[r.pos_of_pair.long()], want[0][r.pos_of_pair.long()])
