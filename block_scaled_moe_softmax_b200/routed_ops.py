@@ -12,8 +12,9 @@ gradients (the ``moe_mx_*`` entry points of the same names in include/moe_mx.h).
     dg, dw1, _ = linear_backward(dh, g, w1, preact=z, activation="swiglu", routing=r)
     dx = dispatch_backward(dg, r)
 
-Gradients are explicit calls, as everything in the library is: results carry no autograd history.  Tensors are contiguous CUDA tensors of
-one device; a call is enqueued on ``stream`` (a torch.cuda.Stream or a raw handle; default: the current
+Gradients are explicit calls, as everything in the library is: results carry no autograd history.  A call
+on a tensor that requires a gradient, with autograd recording, warns (once a place); under
+``torch.no_grad()`` it is silent.  Tensors are contiguous CUDA tensors of one device; a call is enqueued on ``stream`` (a torch.cuda.Stream or a raw handle; default: the current
 stream of the tensors' device) and allocates only what it returns and its workspace, from torch's
 allocator, as under ``with torch.cuda.stream(stream)``.  Wrong types, shapes or
 devices raise TypeError or ValueError before anything is enqueued.  Output buffers may be passed in
@@ -27,6 +28,7 @@ e.g. once a step.
 from __future__ import annotations
 
 import functools
+import warnings
 from typing import NamedTuple
 
 import torch
@@ -64,6 +66,13 @@ def _tensor(t, name, device, dtype=None, shape=None):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     raise ValueError(f"{name} is on {t.device}, not on {'the CPU' if device < 0 else f'cuda:{device}'}")
+
+
+def _no_history(name, level=3):
+    """Warns that a call's result is detached from an input that requires a gradient."""
+    if torch.is_grad_enabled():
+        warnings.warn(f"{name}: an input requires a gradient, but the result carries no autograd history; call "
+                      "the gradient yourself, or under torch.no_grad() to say so", stacklevel=level)
 
 
 def _device(t, name):
@@ -159,6 +168,8 @@ def route_group(router_logits: torch.Tensor, top_k: int, stream=None) -> Routing
     E = _matrix(router_logits, "router_logits", dev, dtype=torch.float32)
     T = router_logits.shape[0]
     on = _on(router_logits, dev, stream)
+    if router_logits.requires_grad:
+        _no_history("route_group")
     rows = max_grouped_rows(T * top_k, E)
     new = lambda *shape, dtype=torch.int32: _empty(shape, dtype, router_logits, stream)  # noqa: E731
     ids, w = new(T, top_k), new(T, top_k, dtype=torch.float32)
@@ -178,6 +189,8 @@ def dispatch(x: torch.Tensor, routing: Routing, out: torch.Tensor | None = None,
     H = _matrix(x, "x", dev, T)
     on = _on(x, dev, stream)
     code = _type(x, "x")
+    if x.requires_grad:
+        _no_history("dispatch")
     out = _out(out, (routing.rows, H), x.dtype, x, dev, "out", stream)
     _call("moe_mx_dispatch", x.data_ptr(), T, H, k, routing.pos_of_pair.data_ptr(), routing.rows, code, out.data_ptr(),
           on)
@@ -190,6 +203,8 @@ def _combine(grouped, routing, w, out_dtype, out, stream):
     H = _matrix(grouped, "grouped", dev, routing.rows)
     on = _on(grouped, dev, stream)
     code = _type(grouped, "grouped")
+    if grouped.requires_grad or (w is not None and w.requires_grad):
+        _no_history("dispatch_backward" if w is None else "combine", 4)
     if out is not None:
         out_dtype = out.dtype
     out = _out(out, (T, H), out_dtype or grouped.dtype, grouped, dev, "out", stream)
@@ -274,6 +289,9 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
     dev = _device(x, "x")
     E, rows, N, K, act, cols, counts, pad = _linear_sizes(x, w, activation, routing, dev)
     on = _on(x, dev, stream)
+    if x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad) or \
+            (residual is not None and residual.requires_grad):
+        _no_history("linear")
     if bias is not None:
         _tensor(bias, "bias", dev, torch.float32, (E, N) if E else (N,))
     if out is not None:

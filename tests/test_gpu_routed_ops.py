@@ -3,6 +3,7 @@ import math
 import os
 import subprocess
 import sys
+import warnings
 
 import pytest
 import torch
@@ -861,3 +862,27 @@ def test_outputs_over_any_input_are_refused():
     assert torch.equal(both, want[1])
     moe_mx.moe_mx_combine_backward(xs, y, r.rows, M, 8, k, r.pos_of_pair, r.topk_w, None, 0, 1, 1, y, None, None)
     assert torch.equal(y[r.pos_of_pair.long()], want[0][r.pos_of_pair.long()])
+
+
+def test_results_without_history_are_announced():
+    r = ref.make_routing(8, 4, 2, 170)
+    x, w, b = rnd((8, 64), BF, 171), rnd((32, 64), BF, 172), rnd((32,), F, 173)
+    logits, g = rnd((8, 4), F, 174), rnd((r.rows, 64), BF, 175)
+    calls = [("linear", lambda: ops.linear(x, w, b), x), ("linear", lambda: ops.linear(x, w, b), w),
+             ("linear", lambda: ops.linear(x, w, b), b), ("dispatch", lambda: ops.dispatch(x, r), x),
+             ("combine", lambda: ops.combine(g, r), g), ("combine", lambda: ops.combine(g, r), r.topk_w),
+             ("route_group", lambda: ops.route_group(logits, 2), logits)]
+    for name, call, leaf in calls:
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            want = call()  # nothing requires a gradient
+            leaf.requires_grad_()
+            with torch.no_grad():
+                call()
+        with pytest.warns(UserWarning, match=f"{name}.*no autograd history") as seen:
+            got = call()
+        assert seen[0].filename == __file__
+        leaf.requires_grad_(False)
+        if name != "dispatch":  # whose padding rows are not written
+            got, want = (got.pos_of_pair, want.pos_of_pair) if name == "route_group" else (got, want)
+            assert torch.equal(got, want) and not got.requires_grad
