@@ -95,7 +95,11 @@ def _on(t, device, stream):
         raise ValueError(f"tensors must be on a CUDA device, not {t.device}")
     if stream is None:
         return _raw_stream(device)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+    if isinstance(stream, int):
+        return stream
+    if stream.device_index != device:
+        raise ValueError(f"stream is one of cuda:{stream.device_index}, the tensors are on cuda:{device}")
+    return stream.cuda_stream
 
 
 # The current stream's handle without a Stream object around it (2 us less a call).
@@ -258,7 +262,11 @@ def _linear_sizes(x, w, activation, routing, dev):
     if x.dtype is not torch.bfloat16 and x.dtype is not torch.float16:
         raise TypeError(f"x has type {x.dtype}; bfloat16 and float16 are supported")
     _tensor(w, "w", dev, x.dtype)
-    E = 0 if routing is None else routing.counts.shape[0]
+    E = 0
+    if routing is not None:
+        E = _tensor(routing.counts, "counts", dev, torch.int32).numel()
+        if E == 0:
+            raise ValueError("the routing has no experts")
     shape = w.shape
     if len(shape) != (3 if E else 2) or shape[-1] != K or (E and shape[0] != E):
         raise ValueError(f"x {tuple(x.shape)} and w {tuple(shape)}: need [rows, K] and "
@@ -289,20 +297,22 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
     dev = _device(x, "x")
     E, rows, N, K, act, cols, counts, pad = _linear_sizes(x, w, activation, routing, dev)
     on = _on(x, dev, stream)
-    if x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad) or \
-            (residual is not None and residual.requires_grad):
-        _no_history("linear")
     if bias is not None:
         _tensor(bias, "bias", dev, torch.float32, (E, N) if E else (N,))
     if out is not None:
         out_dtype = out.dtype
     elif out_dtype is None:
         out_dtype = x.dtype if residual is None else residual.dtype
+    if out_dtype is not x.dtype and out_dtype is not torch.float32:
+        raise TypeError(f"out has type {out_dtype}; {x.dtype} (x's) and float32 are supported")
     out = _out(out, (rows, cols), out_dtype, x, dev, "out", stream)
     if residual is not None:
         _tensor(residual, "residual", dev, out_dtype, (rows, cols))
     if preact is not None:
         _tensor(preact, "preact", dev, x.dtype, (rows, N))
+    if x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad) or \
+            (residual is not None and residual.requires_grad):
+        _no_history("linear")
     dt, ot = _type(x, "x"), _type(out, "out")
     need = _linear_workspace(E, rows, N, K, dt, act, ot)
     ws = _empty((need,), torch.uint8, x, stream) if need else None
@@ -321,6 +331,8 @@ def linear_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, preact
     E, rows, N, K, act, cols, counts, pad = _linear_sizes(x, w, activation, routing, dev)
     on = _on(x, dev, stream)
     _tensor(dout, "dout", dev, None, (rows, cols))
+    if dout.dtype is not x.dtype and dout.dtype is not torch.float32:
+        raise TypeError(f"dout has type {dout.dtype}; {x.dtype} (x's) and float32 are supported")
     if act:
         _tensor(preact, "preact", dev, x.dtype, (rows, N))
     elif preact is not None:

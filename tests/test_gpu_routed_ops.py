@@ -886,3 +886,13 @@ def test_results_without_history_are_announced():
         if name != "dispatch":  # whose padding rows are not written
             got, want = (got.pos_of_pair, want.pos_of_pair) if name == "route_group" else (got, want)
             assert torch.equal(got, want) and not got.requires_grad
+
+
+def test_types_that_do_not_go_together_are_type_errors():
+    x, w = rnd((8, 64), BF, 180), rnd((16, 64), BF, 181)
+    for kw in (dict(out_dtype=HF), dict(out=rnd((8, 16), HF, 182)), dict(residual=rnd((8, 16), HF, 183)),
+               dict(out_dtype=torch.float64)):
+        with pytest.raises(TypeError, match="out has type"):
+            ops.linear(x, w, **kw)
+    with pytest.raises(TypeError, match="dout has type"):
+        ops.linear_backward(rnd((8, 16), HF, 184), x, w)

@@ -1,5 +1,6 @@
 """Refusals of the routed operators, on the host: nothing here reaches a device."""
 import ctypes
+import types
 
 import pytest
 import torch
@@ -148,3 +149,17 @@ def test_products_of_2_to_the_31_values_are_not_split(lib):
             assert M * N >= 1 << 31
             assert lib.moe_mx_linear_workspace(0, M, N, K, 0, 0, 0) < 4 * M * N
     assert lib.moe_mx_linear_workspace(0, 2048, 2560, 14336, 0, 0, 0) >= 2 * 4 * 2048 * 2560  # split, in 240 tiles
+
+
+def test_wrappers_refuse_an_empty_routing_and_other_devices_streams():
+    r = _cpu_routing()
+    x = torch.zeros(r.rows, 64, dtype=torch.bfloat16)
+    none = r._replace(counts=torch.zeros(0, dtype=torch.int32), pad_offsets=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="no experts"):  # not a dense product over the padding too
+        ops.linear(x, torch.zeros(16, 64, dtype=torch.bfloat16), routing=none)
+    with pytest.raises(TypeError, match="counts"):
+        ops.linear(x, torch.zeros(4, 16, 64, dtype=torch.bfloat16), routing=r._replace(counts=[1, 2, 3, 4]))
+    other = types.SimpleNamespace(cuda_stream=1, device_index=1)
+    with pytest.raises(ValueError, match="stream"):
+        ops._on(x, 0, other)
+    assert ops._on(x, 1, other) == 1
