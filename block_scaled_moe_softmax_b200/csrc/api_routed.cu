@@ -254,6 +254,21 @@ int64_t moe_mx_linear_backward_workspace(int num_experts, int64_t rows, int N, i
     return linear_backward_workspace(num_experts, rows, N, K, activation, dtype, dout_dtype);
 }
 
+int moe_mx_debug_linear_plan(int which, int num_experts, int64_t rows, int N, int K, int dtype, int activation,
+                             int io_dtype, int32_t *plan)
+{
+    clear_error();
+    const LinearSizes z{rows, num_experts, N, K, activation};
+    if (int rc = check_linear(z, dtype, io_dtype, which ? "dout_dtype" : "out_dtype"))
+        return rc;
+    if (which < 0 || which > 2)
+        return fail(MOE_MX_ERR_INVALID_ARG, "which=%d must be in [0, 2]", which);
+    if (!plan)
+        return fail(MOE_MX_ERR_INVALID_ARG, "plan is NULL");
+    linear_plan(which, num_experts, rows, N, K, activation, dtype, io_dtype, plan);
+    return MOE_MX_OK;
+}
+
 int moe_mx_linear(const void *x, const void *w, const float *bias, const void *residual, const int32_t *counts,
                   const int32_t *pad_offsets, int num_experts, int64_t rows, int N, int K, int dtype, int activation,
                   int out_dtype, void *out, void *preact, void *workspace, int64_t workspace_bytes, void *stream)

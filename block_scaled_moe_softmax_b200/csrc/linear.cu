@@ -2056,6 +2056,18 @@ int64_t linear_backward_workspace(int E, int64_t M, int N, int K, int act, int t
     return plan_backward(E, M, N, K, act, type, dout_type).bytes;
 }
 
+void linear_plan(int which, int E, int64_t M, int N, int K, int act, int type, int io_type, int *o)
+{
+    if (which == 0 && E == 0 && is_small(M, N, K, act == kActSwiglu)) {
+        o[0] = o[1] = o[2] = o[3] = 0;
+        return;
+    }
+    const Plan p = which == 0   ? plan_linear(E, M, N, K, act, type, io_type == kTypeF32).p
+                   : which == 1 ? plan_backward(E, M, N, K, act, type, io_type).dx
+                                : plan_backward(E, M, N, K, act, type, io_type).dw;
+    o[0] = p.bn, o[1] = p.tok, o[2] = p.splits, o[3] = p.sum;
+}
+
 int launch_linear(const LinearArgs &a, cudaStream_t s)
 {
     if (a.E == 0 && is_small(a.M, a.N, a.K, a.act == kActSwiglu)) {

@@ -58,6 +58,9 @@ struct LinearBackwardArgs {
 };
 int64_t linear_workspace(int E, int64_t M, int N, int K, int act, int type, int out_type);
 int64_t linear_backward_workspace(int E, int64_t M, int N, int K, int act, int type, int dout_type);
+// How linear (0), its dx (1) or dw (2) runs: columns of a tile (0: the few-row kernel), tokens of one (0: a tile
+// has 256 rows), splits of k, and whether chains are summed in registers.
+void linear_plan(int which, int E, int64_t M, int N, int K, int act, int type, int io_type, int *o);
 // MOE_MX_OK or a negative status (text recorded).
 int launch_linear(const LinearArgs &a, cudaStream_t s);
 int launch_linear_backward(const LinearBackwardArgs &a, cudaStream_t s);

@@ -81,6 +81,7 @@ SIGNATURES = {
     "moe_mx_linear_backward_workspace": (_I64, [_I, _I64] + [_I] * 5),
     "moe_mx_linear_status": (_I, [_I, _P]),
     "moe_mx_debug_linear_watchdog": (_I, [_I, _I, _P]),
+    "moe_mx_debug_linear_plan": (_I, [_I, _I, _I64] + [_I] * 5 + [_P]),
 }
 STAGES = ("route", "gather", "fc1", "fc2", "combine")
 
@@ -310,6 +311,13 @@ def moe_mx_linear_backward(dout, x, w, preact, counts, pad_offsets, num_experts:
 def moe_mx_linear_status(device: int, stream=None) -> int:
     """Returns the status code (does not raise on MOE_MX_ERR_TIMEOUT)."""
     return load_library().moe_mx_linear_status(device, _stream(stream))
+
+
+def moe_mx_debug_linear_plan(which: int, num_experts: int, rows: int, N: int, K: int, dtype: int, activation: int,
+                             io_dtype: int) -> tuple:
+    plan = (ctypes.c_int32 * 4)()
+    _check(load_library().moe_mx_debug_linear_plan(which, num_experts, rows, N, K, dtype, activation, io_dtype, plan))
+    return tuple(plan)
 
 
 def moe_mx_debug_linear_watchdog(device: int, timeout_us: int, stream=None) -> None:

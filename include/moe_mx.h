@@ -606,6 +606,15 @@ MOE_MX_API int64_t moe_mx_linear_backward_workspace(int num_experts, int64_t row
 MOE_MX_API int moe_mx_linear_status(int device, void *stream);
 
 /*
+ * Test-only: how a product of these sizes runs (host arithmetic).  which: 0 moe_mx_linear, 1 dx and 2 dw of
+ * moe_mx_linear_backward; io_dtype: out_dtype or dout_dtype.  plan[0]: columns of a tile, 0 for the kernel
+ * of a few rows; plan[1]: tokens of a tile at most, 0 where a tile has 256 rows; plan[2]: splits of K;
+ * plan[3]: 1 if chains of K are summed in registers (float32 outputs).  Errors: INVALID_ARG.
+ */
+MOE_MX_API int moe_mx_debug_linear_plan(int which, int num_experts, int64_t rows, int N, int K, int dtype,
+                                        int activation, int io_dtype, int32_t *plan);
+
+/*
  * Self-test of that report: launch one kernel on `device` that waits on a device flag nothing sets, with
  * a wait limit of timeout_us microseconds.  The wait gives up, the kernel records it in the word that
  * moe_mx_linear_status reads and returns.  Nothing faults or traps.  Errors: INVALID_ARG, CUDA.
