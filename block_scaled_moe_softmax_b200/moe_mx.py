@@ -254,7 +254,8 @@ def moe_mx_get_stage_times(handle: int) -> dict:
 
 
 # ------------------------------------------------------------------ routed operators
-# (block_scaled_moe_softmax_b200.routed_ops calls these on torch tensors)
+# One function an entry point, as above: pointers or tensors, unchecked but for the library's own checks.
+# block_scaled_moe_softmax_b200.routed_ops makes the same calls on checked torch tensors.
 def moe_mx_dispatch(x, num_tokens: int, hidden: int, top_k: int, pos_of_pair, rows: int, dtype: int, grouped,
                     stream=None) -> None:
     _check(load_library().moe_mx_dispatch(_ptr(x), num_tokens, hidden, top_k, _ptr(pos_of_pair), rows, dtype,

@@ -896,3 +896,36 @@ def test_types_that_do_not_go_together_are_type_errors():
             ops.linear(x, w, **kw)
     with pytest.raises(TypeError, match="dout has type"):
         ops.linear_backward(rnd((8, 16), HF, 184), x, w)
+
+
+def test_the_binding_makes_the_same_calls():
+    """The entry points by their names, on raw arguments, against routed_ops."""
+    T, E, k, H, N = 50, 6, 2, 72, 40
+    r = ref.make_routing(T, E, k, 190)
+    x, w, b = rnd((T, H), BF, 191), rnd((E, N, H), BF, 192), rnd((E, N), F, 193)
+    live = r.pos_of_pair.long()
+    g = torch.zeros(r.rows, H, dtype=BF, device="cuda")
+    moe_mx.moe_mx_dispatch(x, T, H, k, r.pos_of_pair, r.rows, 0, g)
+    assert torch.equal(g[live], ops.dispatch(x, r)[live])
+    y, z = torch.zeros(r.rows, N, dtype=F, device="cuda"), torch.zeros(r.rows, N, dtype=BF, device="cuda")
+    need = moe_mx.moe_mx_linear_workspace(E, r.rows, N, H, 0, moe_mx.MOE_MX_LINEAR_SILU, 1)
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    moe_mx.moe_mx_linear(g, w, b, None, r.counts, r.pad_offsets, E, r.rows, N, H, 0, moe_mx.MOE_MX_LINEAR_SILU, 1, y, z,
+                         ws, need)
+    want_z = torch.zeros_like(z)
+    assert torch.equal(y[live], ops.linear(g, w, b, activation="silu", routing=r, out_dtype=F, preact=want_z)[live])
+    assert torch.equal(z, want_z)
+    out = torch.empty(T, N, dtype=BF, device="cuda")
+    moe_mx.moe_mx_combine(y, r.rows, T, N, k, r.pos_of_pair, r.topk_w, 1, 0, out)
+    assert torch.equal(out, ops.combine(y, r, out_dtype=BF))
+    dy, dw, dl = torch.zeros_like(y), torch.empty(T, k, device="cuda"), torch.empty(T, E, device="cuda")
+    moe_mx.moe_mx_combine_backward(out, y, r.rows, T, N, k, r.pos_of_pair, r.topk_w, r.topk_ids, E, 1, 0, dy, dw, dl)
+    want = ops.combine_backward(out, y, r, num_experts=E)
+    assert torch.equal(dy[live], want[0][live]) and torch.equal(dw, want[1]) and torch.equal(dl, want[2])
+    need = moe_mx.moe_mx_linear_backward_workspace(E, r.rows, N, H, 0, moe_mx.MOE_MX_LINEAR_SILU, 1)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    dx, dwt, db = torch.zeros_like(g), torch.empty_like(w), torch.empty_like(b)
+    moe_mx.moe_mx_linear_backward(dy, g, w, z, r.counts, r.pad_offsets, E, r.rows, N, H, 0, moe_mx.MOE_MX_LINEAR_SILU, 1,
+                                  dx, dwt, db, ws, need)
+    want = ops.linear_backward(dy, g, w, z, "silu", r, bias_grad=True)
+    assert torch.equal(dx[live], want[0][live]) and torch.equal(dwt, want[1]) and torch.equal(db, want[2])
