@@ -1060,6 +1060,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if constexpr (kSum) {
                 // columns lc .. of D (gated: and the same of the up half) summed over the chains
                 constexpr int kChunks = BN / 64;
+                const bool gated = kChunks % 2 == 0 && g.gated; // the plan gates no tile of 192 columns
                 uint32_t sum[kChunks][32];
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c)
@@ -1068,7 +1069,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         sum[c][x] = 0u;
                 // chunk c's first accumulator column: this warp's half, or its gate and up columns
                 auto acc_col = [&](int c) {
-                    return g.gated ? (c % (kChunks / 2)) * 32 + half * (BN / 4) + (c >= kChunks / 2 ? BN / 2 : 0)
+                    return gated ? (c % (kChunks / 2)) * 32 + half * (BN / 4) + (c >= kChunks / 2 ? BN / 2 : 0)
                                    : half * (BN / 2) + c * 32;
                 };
                 for (int kb = 0; ok && kb < t.nkb; kb += kChain) {
@@ -1091,16 +1092,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (!ok)
                     break;
-                if (g.gated) {
-                    if constexpr (kChunks % 2 == 0) {
+                if (gated) {
 #pragma unroll
-                        for (int c = 0; c < kChunks / 2; ++c) {
-                            float z[32], up[32];
-                            const int lc = half * cols + c * 32;
-                            turn_columns(sum[c], z);
-                            turn_columns(sum[c + kChunks / 2], up);
-                            finish_column<true>(ep, d_off, row32, t.n0 + lc + lane, column_rows(lc), z, up);
-                        }
+                    for (int c = 0; c < kChunks / 2; ++c) {
+                        float z[32], up[32];
+                        const int lc = half * cols + c * 32;
+                        turn_columns(sum[c], z);
+                        turn_columns(sum[c + kChunks / 2], up);
+                        finish_column<true>(ep, d_off, row32, t.n0 + lc + lane, column_rows(lc), z, up);
                     }
                 } else {
 #pragma unroll
