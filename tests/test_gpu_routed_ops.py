@@ -929,3 +929,54 @@ def test_the_binding_makes_the_same_calls():
                                   dx, dwt, db, ws, need)
     want = ops.linear_backward(dy, g, w, z, "silu", r, bias_grad=True)
     assert torch.equal(dx[live], want[0][live]) and torch.equal(dwt, want[1]) and torch.equal(db, want[2])
+
+
+# ---------------------------------------------------------------- float32 outputs, each held to its own sums
+@pytest.mark.parametrize("M,N,K,act,chain", [
+    (16, 4096, 7168, "none", 8), (8, 4096, 7168, "swiglu", 8), (1, 384, 7168, "none", 8), (9, 1000, 20000, "none", 8),
+    (24, 1024, 5000, "none", 16), (50, 1000, 2048, "none", 16), (16, 2048, 20000, "swiglu", 8),
+    (64, 2048, 1984, "none", 16)])
+def test_few_rows_in_float32_keep_short_chains(M, N, K, act, chain):
+    """Few rows: a warp sums at most 256 of k, 16 additions of 16 products, in one tensor-core chain, and longer
+    slices in chains of 128 (8 additions) or 64.  An addition truncates by half a step in the mean, 2^-24 of the
+    running sum at most; the running sums r_1 .. r_n of a chain of n random additions correlate as min(i, j), so
+    that the chain is off by sqrt(sum min(i, j) / n) = sqrt((n + 1) (2 n + 1) / 6) such parts of its norm, and the
+    whole by the same of its own.  Joining at most 64 chains of a warp, 8 warps and 8 CTAs: 80 roundings
+    of 2^-24 / sqrt(3) of a growing sum.  The last case has more multiplications (260 M) than the few-row kernel
+    takes: a tile product in 8 splits of 4 blocks, 16 additions too."""
+    plan = moe_mx.moe_mx_debug_linear_plan(0, 0, M, N, K, 0, ops.ACTIVATIONS[act], 1)
+    assert plan == ((256, 64, 8, 0) if (M, N, K) == (64, 2048, 1984) else (0, 0, 0, 0))
+    x, w, b, _, _ = _linear_inputs(M, N, K, BF, F, act, True, False, 200)
+    got = ops.linear(x, w, b, activation=act, out_dtype=F)
+    want = ref.linear64(x, w, b, None, act)[0]
+    tol = 2.0 ** -24 * math.sqrt((chain + 1) * (2 * chain + 1) / 6 + 80 / 3 / 2)
+    tol *= math.sqrt(2) if act == "swiglu" else 1  # two such sums in each output
+    rel = float((got.to(ref.F64) - want).norm() / want.norm())
+    assert rel <= tol, f"{rel:.2e} of {tol:.2e}"
+
+
+def test_layer_outputs_each_to_their_own_roundings():
+    """As test_layer_and_its_gradients_together, each result to the number of its roundings in a row (each at most
+    u, independent: sqrt(n) u in norm): out h, y, out; dw2 dy, h, dw2; dw1 dy, dh, z, dz, dw1; db1 dy, dh, z; the
+    router's through y (h, y), dz and the result, with a condition of 2 for the difference in the softmax's
+    gradient; dx all of dw1's and dg, and the sum's.  float32 logits: one chain of 12 additions."""
+    p, k = _stage_inputs()
+    got, r = _layer(p, k)
+    leaf = {n: t.to(ref.F64).requires_grad_() for n, t in p.items() if n != "dout"}
+    logits = leaf["x"] @ leaf["wr"].t() + leaf["br"]
+    ids = r.topk_ids.long()
+    w = torch.softmax(logits.gather(1, ids), 1)
+    z = torch.einsum("th,enh->ten", leaf["x"], leaf["w1"]) + leaf["b1"]
+    y = torch.einsum("tei,ehi->teh", ref.act64(z, "swiglu"), leaf["w2"])
+    out = (y[torch.arange(ids.shape[0], device="cuda")[:, None], ids] * w[..., None]).sum(1)
+    names = ["x", "wr", "br", "w1", "b1", "w2"]
+    grads = dict(zip(names, torch.autograd.grad(out, [leaf[n] for n in names], p["dout"].to(ref.F64))))
+    u = ref.u(BF)
+    for name, g, want, tol in (
+            ("logits", got["logits"], logits, 2.0 ** -24 * math.sqrt(13 * 25 / 6 + 2)),
+            ("out", got["out"], out, math.sqrt(3) * u), ("w2", got["dw2"], grads["w2"], math.sqrt(3) * u),
+            ("w1", got["dw1"], grads["w1"], math.sqrt(5) * u), ("b1", got["db1"], grads["b1"], math.sqrt(3) * u),
+            ("wr", got["dwr"], grads["wr"], 2 * math.sqrt(4) * u), ("br", got["dbr"], grads["br"], 2 * math.sqrt(2) * u),
+            ("x", got["dxr"].to(ref.F64) + got["dxe"].to(ref.F64), grads["x"], math.sqrt(8) * u)):
+        rel = float((g.to(ref.F64) - want.detach()).norm() / want.detach().norm())
+        assert rel <= tol, f"{name}: relative error {rel:.2e} of {tol:.2e}"
