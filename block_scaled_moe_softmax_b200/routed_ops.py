@@ -179,8 +179,10 @@ def route_group(router_logits: torch.Tensor, top_k: int, stream=None) -> Routing
     ids, w = new(T, top_k), new(T, top_k, dtype=torch.float32)
     counts, pad, pos, pair = new(E), new(E + 1), new(T * top_k), new(rows)
     if T == 0:
-        counts.zero_()
-        pad.zero_()
+        # on the call's stream, whose pool they are of
+        with torch.cuda.stream(torch.cuda.ExternalStream(on, device=router_logits.device)):
+            counts.zero_()
+            pad.zero_()
     with torch.cuda.device(dev):
         moe_mx.moe_mx_route_group_noalloc(router_logits, T, E, top_k, ids, w, counts, pad, pair, pos, on)
     return Routing(ids, w, counts, pad, pos, rows)

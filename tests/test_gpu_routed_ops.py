@@ -980,3 +980,24 @@ def test_layer_outputs_each_to_their_own_roundings():
             ("x", got["dxr"].to(ref.F64) + got["dxe"].to(ref.F64), grads["x"], math.sqrt(8) * u)):
         rel = float((g.to(ref.F64) - want.detach()).norm() / want.detach().norm())
         assert rel <= tol, f"{name}: relative error {rel:.2e} of {tol:.2e}"
+
+
+def test_no_tokens_on_another_stream():
+    """counts and pad_offsets are zeroed on the call's stream: zeros from another could come before a write still
+    to come to the memory they got."""
+    s, E = torch.cuda.Stream(), 4096 // 4 - 1  # both in blocks of one size
+    torch.cuda.synchronize()
+    for handle in (s, s.cuda_stream):
+        with torch.cuda.stream(s):
+            old = [torch.empty(E + i % 2, dtype=torch.int32, device="cuda") for i in range(12)]
+            torch.cuda._sleep(20_000_000)
+            for t in old:
+                t.fill_(7)
+            del t, old  # freed on s, their fills still to come
+        r = ops.route_group(torch.empty(0, E, device="cuda"), 2, stream=handle)
+        torch.cuda.synchronize()
+        assert not r.counts.any() and not r.pad_offsets.any()
+    r = ops.route_group(torch.empty(0, E, device="cuda"), 2, stream=0)  # the default stream by its handle
+    assert not r.counts.any() and not r.pad_offsets.any()
+    x = rnd((4, 72), BF, 210)
+    assert torch.equal(ops.linear(x, x, stream=0), ops.linear(x, x))
