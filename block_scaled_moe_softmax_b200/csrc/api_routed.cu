@@ -146,7 +146,7 @@ int moe_mx_dispatch(const void *x, int num_tokens, int hidden, int top_k, const 
 {
     clear_error();
     int rc = check_permute(num_tokens, hidden, top_k, rows, dtype);
-    if (rc || num_tokens == 0)
+    if (rc || num_tokens == 0 || rows == 0)
         return rc;
     int dev;
     if ((rc = device_of(x, "x", &dev)) ||
@@ -177,7 +177,7 @@ int moe_mx_combine(const void *grouped, int64_t rows, int num_tokens, int hidden
         return MOE_MX_OK;
     int dev;
     if ((rc = device_of(out, "out", &dev)) ||
-        (rc = check_ptr(grouped, dev, "grouped")) || (rc = check_ptr(pos_of_pair, dev, "pos_of_pair")) ||
+        (rows && (rc = check_ptr(grouped, dev, "grouped"))) || (rc = check_ptr(pos_of_pair, dev, "pos_of_pair")) ||
         (topk_w && (rc = check_ptr(topk_w, dev, "topk_w"))))
         return rc;
     const size_t T = num_tokens, pairs = T * top_k * 4;
@@ -213,8 +213,8 @@ int moe_mx_combine_backward(const void *dout, const void *grouped, int64_t rows,
     int dev;
     if ((rc = device_of(dout, "dout", &dev)) ||
         (rc = check_ptr(pos_of_pair, dev, "pos_of_pair")) || (rc = check_ptr(topk_w, dev, "topk_w")) ||
-        (dgrouped && (rc = check_ptr(dgrouped, dev, "dgrouped"))) ||
-        ((dtopk_w || dlogits) && (rc = check_ptr(grouped, dev, "grouped"))) ||
+        (dgrouped && rows && (rc = check_ptr(dgrouped, dev, "dgrouped"))) ||
+        ((dtopk_w || dlogits) && rows && (rc = check_ptr(grouped, dev, "grouped"))) ||
         (dtopk_w && (rc = check_ptr(dtopk_w, dev, "dtopk_w"))) ||
         (dlogits && ((rc = check_ptr(dlogits, dev, "dlogits")) || (rc = check_ptr(topk_ids, dev, "topk_ids")))))
         return rc;

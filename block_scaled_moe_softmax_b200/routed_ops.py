@@ -14,7 +14,8 @@ gradients (the ``moe_mx_*`` entry points of the same names in include/moe_mx.h).
 
 Gradients are explicit calls, as everything in the library is: results carry no autograd history.  A call
 on a tensor that requires a gradient, with autograd recording, warns (once a place); under
-``torch.no_grad()`` it is silent.  Tensors are contiguous CUDA tensors of one device; a call is enqueued on ``stream`` (a torch.cuda.Stream or a raw handle; default: the current
+``torch.no_grad()`` it is silent.  Tensors are contiguous CUDA tensors of one device that start on 16 bytes
+(MoeMxError else); a call is enqueued on ``stream`` (a torch.cuda.Stream or a raw handle; default: the current
 stream of the tensors' device) and allocates only what it returns and its workspace, from torch's
 allocator, as under ``with torch.cuda.stream(stream)``.  Wrong types, shapes or
 devices raise TypeError or ValueError before anything is enqueued.  Output buffers may be passed in

@@ -485,7 +485,8 @@ MOE_MX_API int moe_mx_route_group_noalloc(const float *router_logits, int num_to
  *
  * Grouped layout: grouped buffers have `rows` rows (at least pad_offsets[E]); expert e's rows are
  * pad_offsets[e] .. pad_offsets[e] + counts[e] - 1, pad_offsets[e] being multiples of 128 in
- * ascending order.  The other rows are padding: never read into a result, never written.
+ * ascending order.  The other rows are padding: never read into a result, never written.  rows may be 0
+ * (a shard that no pair goes to); grouped buffers may then be NULL.
  * Dimensions (hidden, N, K): 1..2^20, odd ones included (multiples of 8 are fastest).
  * ------------------------------------------------------------------------- */
 

@@ -1001,3 +1001,22 @@ def test_no_tokens_on_another_stream():
     assert not r.counts.any() and not r.pad_offsets.any()
     x = rnd((4, 72), BF, 210)
     assert torch.equal(ops.linear(x, x, stream=0), ops.linear(x, x))
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_a_shard_that_no_pair_goes_to(dtype):
+    """A grouped layout of no rows: nothing is moved, sums and gradients are zero."""
+    T, E, k, H = 5, 4, 2, 40
+    i32 = lambda *s, v=0: torch.full(s, v, dtype=torch.int32, device="cuda")  # noqa: E731
+    r = ops.Routing(i32(T, k), torch.rand(T, k, device="cuda"), i32(E), i32(E + 1), i32(T * k, v=-1), 0)
+    x, none = rnd((T, H), dtype, 220), torch.empty(0, H, dtype=dtype, device="cuda")
+    assert ops.dispatch(x, r).shape == (0, H)
+    for out in (ops.combine(none, r), ops.dispatch_backward(none, r)):
+        assert out.shape == (T, H) and not out.any()
+    dy, dw, dlogits = ops.combine_backward(x, none, r, num_experts=E)
+    assert dy.shape == (0, H) and not dw.any() and not dlogits.any()
+    if dtype == BF:
+        w = rnd((E, 24, H), BF, 221)
+        assert ops.linear(none, w, routing=r).shape == (0, 24)
+        dx, dw, db = ops.linear_backward(none.new_empty(0, 24), none, w, routing=r, bias_grad=True)
+        assert dx.shape == (0, H) and not dw.any() and not db.any()
