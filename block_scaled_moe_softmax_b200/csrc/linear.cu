@@ -22,7 +22,9 @@ namespace moe_mx {
 namespace {
 
 // ---------------------------------------------------------------- activations
-// 1 / (1 + e^-v) to a few ulp (0 once e^-v overflows)
+// 1 / (1 + e^-v) to a few parts in 2^24, and far below 0 as if v were off by a few parts in 2^24 of its own
+// (|v| 2^-23 of the result, as much as rounding v itself moves it): __expf rounds its argument's product with
+// log2(e).  0 once e^-v overflows.
 __device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
 // gelu in its tanh form: 0.5 z (1 + tanh u) = z sigmoid(2u), u = sqrt(2/pi) (z + 0.044715 z^3)
